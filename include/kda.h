@@ -265,6 +265,163 @@ kda_status kda_decode_step(const void *q, const void *k, const void *v, const vo
                            int64_t n_slots, void *out, const kda_shape *shape,
                            int32_t *status, kda_stream_t stream);
 
+/* ------------------------------------------------------------- latent attention
+ *
+ * Attention whose keys and values all come from one latent vector a token, the global
+ * attention layer that hybrid models put between KDA layers ("Kimi K3 深度拆解": three KDA
+ * layers to one latent-attention layer). A token keeps a latent c (512 values) and a shared
+ * key part k_pe (64 values, one for all heads). Two forms of the same attention:
+ *
+ *  expanded (prompts, training): the caller projects c to k_nope and v of every head;
+ *      s_ij = scale q_i . [k_nope_j | k_pe_j],  p = softmax_j(s),  out_i = sum_j p_ij v_j
+ *  absorbed (single and drafted tokens): the caller folds the key projection into the
+ *      query and the value projection into what follows, so the cached vector is the key
+ *      and its latent the value:
+ *      s_j = scale q . [c_j | k_pe_j],  p = softmax_j(s),  out = sum_j p_j c_j
+ *
+ * Scores, softmax statistics and sums are fp32; probabilities and score gradients enter
+ * the tensor cores as bf16. lse is the natural log of the sum of exponentials. A row that
+ * sees no key has out = 0 and lse = -inf (and adds nothing to any gradient).
+ *
+ * Every function takes `status`, an int32 device word or NULL, which receives 1 for a
+ * malformed or too long sequence, 2 for an expired bounded wait and 3 for a page or slot
+ * out of range; it is never cleared (zero it before the calls it should cover;
+ * kda_workspace_status(status, 4, ...) reads it). Nothing is allocated and nothing is kept
+ * between calls; every call may be captured in a CUDA graph. Results do not depend on the
+ * order in which thread blocks run.
+ */
+typedef struct {
+    int32_t B;          /* sequences, when cu_seqlens_q == NULL; 1 otherwise */
+    int32_t H;          /* heads (1 .. 65535) */
+    int64_t Tq, Tk;     /* query and key tokens: of each sequence without cu_seqlens, total
+                           rows of the packed tensors with them */
+    int32_t n_seqs;     /* with cu_seqlens: number of sequences (1 .. 65535), else 0 */
+    int64_t max_q, max_k; /* with cu_seqlens: bounds on a sequence's lengths (0: Tq, Tk); a
+                           longer sequence is skipped and reported */
+    int32_t d_nope, d_pe, d_v; /* 128, 64, 128 */
+    int64_t q_token, q_head;   /* strides in elements, multiples of 8; channels are */
+    int64_t k_token, k_head;   /* contiguous. q [.., d_nope + d_pe], k_nope [.., d_nope], */
+    int64_t pe_token;          /* k_pe [.., d_pe] (no head), v [.., d_v]: k_nope and v may */
+    int64_t v_token, v_head;   /* be views of one [Tk, H, d_nope + d_v] projection */
+    int32_t causal;     /* 1: query i of a sequence sees keys j <= i + (len_k - len_q), the
+                           queries being its last tokens (a cached prefix before them);
+                           0: every key */
+    kda_dtype dtype;    /* KDA_BF16 */
+    float scale;        /* 0 selects 1/sqrt(d_nope + d_pe) */
+} kda_latent_shape;
+
+/*
+ * Expanded form, forward. cu_seqlens_q, cu_seqlens_k: int32 [n_seqs + 1], both or neither,
+ * 0 = c_0 <= c_1 <= ... <= c_n <= Tq (Tk); rows behind c_n belong to no sequence and are
+ * neither read into a result nor written. out [Tq, H, d_v] and lse [Tq, H] fp32 (or NULL)
+ * are contiguous; batched tensors are sequence after sequence.
+ */
+kda_status kda_latent_attn_fwd(const void *q, const void *k_nope, const void *k_pe,
+                               const void *v, const int32_t *cu_seqlens_q,
+                               const int32_t *cu_seqlens_k, void *out, float *lse,
+                               const kda_latent_shape *shape, int32_t *status,
+                               kda_stream_t stream);
+
+/* Bytes of scratch kda_latent_attn_bwd needs (a function of the shape); 0: invalid shape. */
+size_t kda_latent_attn_bwd_workspace_size(const kda_latent_shape *shape);
+
+/*
+ * Gradients of the expanded form: from the forward's inputs, out and lse and d_out
+ * [Tq, H, d_v] (contiguous), writes dq [Tq, H, d_nope + d_pe], dk_nope [Tk, H, d_nope],
+ * dk_pe [Tk, d_pe] (summed over the heads in fp32) and dv [Tk, H, d_v], all contiguous.
+ * Rows behind c_n are not written. The workspace is 256-byte aligned and used only for the
+ * duration of the enqueued work. No atomics: the same inputs give the same bits.
+ */
+kda_status kda_latent_attn_bwd(const void *q, const void *k_nope, const void *k_pe,
+                               const void *v, const void *out, const float *lse,
+                               const void *d_out, const int32_t *cu_seqlens_q,
+                               const int32_t *cu_seqlens_k, void *dq, void *dk_nope,
+                               void *dk_pe, void *dv, const kda_latent_shape *shape,
+                               void *workspace, size_t workspace_bytes, int32_t *status,
+                               kda_stream_t stream);
+
+/*
+ * The paged cache of latent vectors: `n_pages` pages of `page_size` rows, one row a token,
+ * in one contiguous 16-byte aligned tensor.
+ *  KDA_CACHE_BF16  576 bf16: the latent, then k_pe.                          1152 bytes
+ *  KDA_CACHE_E4M3  512 bytes: the latent in 8 bits, in four groups of 128 channels: the
+ *                  e4m3 (finite, round to nearest even) codes of x / 2^e, e the smallest
+ *                  integer in [-120, 120] with max|x| <= 448 * 2^e over the group's finite
+ *                  values; 64 bf16: k_pe as it is; 4 bytes: e + 127 of each group; 12
+ *                  unused bytes, written as zero.                              656 bytes
+ *                  The scales are powers of two, so every stored value is a bf16 number and
+ *                  x / 2^e is not rounded before its code is. A latent value that is not
+ *                  finite is stored as NaN.
+ */
+typedef enum { KDA_CACHE_BF16 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format;
+#define KDA_CACHE_E4M3_ROW_BYTES 656
+
+typedef struct {
+    int64_t n_pages;
+    int32_t page_size;  /* 16, 32, 64 or 128 rows */
+    int32_t d_c, d_pe;  /* 512, 64 */
+    int32_t format;     /* kda_cache_format */
+} kda_latent_cache;
+
+/*
+ * Writes T tokens into the cache: row slots[t] (= page * page_size + offset, int64, device)
+ * gets latent [T, d_c] and k_pe [T, d_pe] of token t (bf16, row strides in elements,
+ * multiples of 8). A negative slot is skipped (padding); one past the cache is skipped and
+ * reported. Slots must be distinct (two tokens of one slot race).
+ */
+kda_status kda_latent_cache_write(const void *latent, int64_t latent_token, const void *k_pe,
+                                  int64_t pe_token, const int64_t *slots, int64_t T,
+                                  void *cache, const kda_latent_cache *cache_shape,
+                                  int32_t *status, kda_stream_t stream);
+
+/*
+ * Reads tokens back: sequence s's tokens starts[s] .. starts[s] + cu[s+1] - cu[s] - 1 (starts
+ * NULL: from 0), found through block_table [n_seqs, table_pages] (int32 page numbers), go to
+ * rows cu[s] .. cu[s+1] - 1 of out [T, d_c + d_pe] bf16 (contiguous). 8-bit values come back
+ * exactly as they are stored. Rows behind cu[n_seqs] are not written; a token whose page is
+ * out of range, or past the table, is read as NaN and reported.
+ */
+kda_status kda_latent_cache_read(const void *cache, const int32_t *block_table,
+                                 int64_t table_pages, const int32_t *cu_seqlens,
+                                 const int32_t *starts, int32_t n_seqs, int64_t T, void *out,
+                                 const kda_latent_cache *cache_shape, int32_t *status,
+                                 kda_stream_t stream);
+
+typedef struct {
+    int32_t N;          /* sequences */
+    int32_t L;          /* query tokens of each (1: plain decode; up to 64 drafted tokens) */
+    int32_t H;          /* heads */
+    int64_t table_pages;/* columns of block_table */
+    kda_dtype dtype;    /* KDA_BF16 */
+    float scale;        /* of the expanded head: 0 selects 1/sqrt(128 + d_pe) */
+} kda_latent_decode_shape;
+
+/* Bytes of scratch kda_latent_decode needs; 0: invalid shape. */
+size_t kda_latent_decode_workspace_size(const kda_latent_decode_shape *shape,
+                                        const kda_latent_cache *cache_shape);
+
+/*
+ * Absorbed form over the paged cache, for single tokens and for drafted ones.
+ *  q           [N, L, H, d_c + d_pe] bf16, contiguous
+ *  block_table int32 [N, table_pages]; entries past a sequence's pages are not read
+ *  seq_lens    int32 [N]: cached tokens of each sequence, its L query tokens (the last ones)
+ *              included; 0 leaves its rows empty
+ *  draft_mask  int64 [N, L] or NULL. Without it query i sees the tokens up to its own,
+ *              position seq_len - L + i. With it, query i sees every token before the L
+ *              last ones and, of those, token j where bit j of draft_mask[n][i] is set (a
+ *              tree of drafted tokens: bits of its ancestors and itself).
+ *  out         [N, L, H, d_c] bf16, contiguous    lse [N, L, H] fp32 or NULL
+ *  workspace   >= kda_latent_decode_workspace_size bytes, 256-byte aligned; calls that share
+ *              one must be ordered on one stream.
+ * A sequence with seq_len < 0 or past its table, or with a page out of range among its own,
+ * has NaN out rows and is reported.
+ */
+kda_status kda_latent_decode(const void *q, const void *cache, const int32_t *block_table,
+                             const int32_t *seq_lens, const int64_t *draft_mask, void *out,
+                             float *lse, const kda_latent_decode_shape *shape,
+                             const kda_latent_cache *cache_shape, void *workspace,
+                             size_t workspace_bytes, int32_t *status, kda_stream_t stream);
+
 /*
  * Synchronises `stream` and reads the device-side status word a previous
  * kda_chunk_fwd (or kda_chunk_bwd) left in `workspace`: KDA_OK, or KDA_ERR_DEVICE

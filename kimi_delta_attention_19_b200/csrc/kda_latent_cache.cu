@@ -1,0 +1,170 @@
+// kda_latent_cache.cu -- the paged latent cache: tokens written into it, in bf16 or with the
+// latent in 8 bits, and read back.
+//
+// An 8-bit row holds, for each 128-channel group of the latent, the e4m3 codes of x / 2^e
+// with e the smallest integer for which the group's largest finite magnitude is at most
+// 448 * 2^e: with amax = m 2^k, 1 <= m < 2, and 448 = 1.75 * 2^8, e = k - 8 + (m > 1.75). A
+// power of two makes x / 2^e exact, so the code's is the only rounding (half a step: 2^-4
+// relative for normal codes), and every stored value, 4 significant bits times 2^e, is a
+// bf16 number: reading back rounds nothing.
+//
+// Bound by memory: 1152 bytes in and 644 out a token. One warp a token, 16 channels a lane,
+// so a group is 8 lanes and its maximum three shuffles.
+#include <cuda_fp8.h>
+
+#include "kda_latent.cuh"
+
+namespace kda {
+namespace latent {
+namespace {
+
+constexpr int kWarps = 8;
+
+// e4m3 codes of two values already divided by their scale; not finite -> NaN
+__device__ __forceinline__ uint32_t codes2(float x, float y) {
+  uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+  if (!isfinite(x)) c |= 0x7f;
+  if (!isfinite(y)) c |= 0x7f00;
+  return c;
+}
+
+__device__ __forceinline__ float2 unpack(uint32_t b) {
+  return make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+}
+
+__global__ void __launch_bounds__(kWarps * 32)
+    cache_write_kernel(const __nv_bfloat16* c, int64_t c_token, const __nv_bfloat16* pe,
+                       int64_t pe_token, const int64_t* slots, int64_t T, CacheArgs cache,
+                       int32_t* status) {
+  const int lane = threadIdx.x % 32;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
+  if (t >= T) return;
+  const int64_t slot = slots[t];
+  if (slot < 0) return;
+  if (slot >= cache.n_pages * cache.page_size) {
+    if (lane == 0 && status != nullptr) atomicExch(status, kDevBadPage);
+    return;
+  }
+  const uint4* src = reinterpret_cast<const uint4*>(c + t * c_token);
+  const uint4* psrc = reinterpret_cast<const uint4*>(pe + t * pe_token);
+  unsigned char* row = const_cast<unsigned char*>(cache.cache) +
+                       slot * (cache.format == KDA_CACHE_BF16 ? DX * 2 : kRow8);
+  if (cache.format == KDA_CACHE_BF16) {
+    uint4* dst = reinterpret_cast<uint4*>(row);
+    const uint4 a = src[lane], b = src[lane + 32];
+    dst[lane] = a;
+    dst[lane + 32] = b;
+    if (lane < 8) dst[64 + lane] = psrc[lane];
+    return;
+  }
+  const uint4 v[2] = {src[2 * lane], src[2 * lane + 1]};
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  uint32_t amax = 0;  // the largest finite magnitude's bits (bf16 order = integer order)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+    if (lo < 0x7f80u && lo > amax) amax = lo;
+    if (hi < 0x7f80u && hi > amax) amax = hi;
+  }
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1)
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7fu) > 0x60u);
+  e = max(-120, min(120, e));
+  const float inv = __int_as_float((127 - e) << 23);
+  uint32_t code[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack(w[2 * i]), y = unpack(w[2 * i + 1]);
+    code[i] = codes2(x.x * inv, x.y * inv) | codes2(y.x * inv, y.y * inv) << 16;
+  }
+  reinterpret_cast<uint4*>(row)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
+  uint32_t exps = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    exps |= static_cast<uint32_t>(__shfl_sync(0xffffffffu, e, 8 * g) + 127) << (8 * g);
+  if (lane < 8) reinterpret_cast<uint4*>(row + kPe8)[lane] = psrc[lane];
+  if (lane == 8) *reinterpret_cast<uint4*>(row + kExp8) = make_uint4(exps, 0, 0, 0);
+}
+
+// Two bf16 values of two e4m3 codes times 2^e (exact)
+__device__ __forceinline__ uint32_t values2(uint32_t codes, float scale) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
+  const float2 f = __half22float2(__half2(h));
+  const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__global__ void __launch_bounds__(kWarps * 32)
+    cache_read_kernel(CacheArgs cache, const int32_t* table, int64_t table_pages,
+                      const int32_t* cu, const int32_t* starts, int n_seqs, int64_t T,
+                      __nv_bfloat16* out, int32_t* status) {
+  const int lane = threadIdx.x % 32;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
+  if (t >= T || t >= cu[n_seqs]) return;
+  int lo = 0, hi = n_seqs;  // the last s in [0, n_seqs) with cu[s] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int64_t first = cu[lo];
+  const int64_t pos = t - first + (starts != nullptr ? starts[lo] : 0);
+  const int64_t col = pos / cache.page_size;
+  uint4* dst = reinterpret_cast<uint4*>(out + t * DX);
+  int64_t page = -1;
+  if (t >= first && pos >= 0 && col < table_pages)
+    page = table[static_cast<int64_t>(lo) * table_pages + col];
+  if (page < 0 || page >= cache.n_pages) {
+    if (lane == 0 && status != nullptr) atomicExch(status, kDevBadPage);
+    const uint4 nan = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+    dst[lane] = nan;
+    dst[lane + 32] = nan;
+    if (lane < 8) dst[64 + lane] = nan;
+    return;
+  }
+  const int64_t slot = page * cache.page_size + pos % cache.page_size;
+  if (cache.format == KDA_CACHE_BF16) {
+    const uint4* row = reinterpret_cast<const uint4*>(cache.cache + slot * DX * 2);
+    const uint4 a = row[lane], b = row[lane + 32];
+    dst[lane] = a;
+    dst[lane + 32] = b;
+    if (lane < 8) dst[64 + lane] = row[64 + lane];
+    return;
+  }
+  const unsigned char* row = cache.cache + slot * kRow8;
+  const uint4 code = reinterpret_cast<const uint4*>(row)[lane];
+  const uint32_t exps = *reinterpret_cast<const uint32_t*>(row + kExp8);
+  const uint32_t e = exps >> (8 * (lane / 8)) & 0xffu;
+  const float scale = __uint_as_float(e << 23);
+  const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[2 * i] = values2(w[i] & 0xffffu, scale);
+    r[2 * i + 1] = values2(w[i] >> 16, scale);
+  }
+  dst[2 * lane] = make_uint4(r[0], r[1], r[2], r[3]);
+  dst[2 * lane + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+  if (lane < 8) dst[64 + lane] = reinterpret_cast<const uint4*>(row + kPe8)[lane];
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const __nv_bfloat16* c, int64_t c_token, const __nv_bfloat16* pe,
+                               int64_t pe_token, const int64_t* slots, int64_t T,
+                               const CacheArgs& cache, int32_t* status, cudaStream_t st) {
+  cache_write_kernel<<<static_cast<unsigned>((T + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(
+      c, c_token, pe, pe_token, slots, T, cache, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const CacheArgs& cache, const int32_t* table, int64_t table_pages,
+                              const int32_t* cu, const int32_t* starts, int n_seqs, int64_t T,
+                              __nv_bfloat16* out, int32_t* status, cudaStream_t st) {
+  cache_read_kernel<<<static_cast<unsigned>((T + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(
+      cache, table, table_pages, cu, starts, n_seqs, T, out, status);
+  return cudaGetLastError();
+}
+
+}  // namespace latent
+}  // namespace kda
