@@ -88,7 +88,7 @@ struct DecodeLatentArgs {
 
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t st);
-size_t decode_workspace(int N, int L, int H);
+size_t decode_workspace(int L, int H);
 cudaError_t launch_latent_decode(const DecodeLatentArgs& a, cudaStream_t st);
 cudaError_t launch_cache_write(const __nv_bfloat16* c, int64_t c_token, const __nv_bfloat16* pe,
                                int64_t pe_token, const int64_t* slots, int64_t T,

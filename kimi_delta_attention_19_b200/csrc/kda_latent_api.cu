@@ -226,7 +226,7 @@ kda_status kda_latent_cache_read(const void* cache, const int32_t* block_table,
 size_t kda_latent_decode_workspace_size(const kda_latent_decode_shape* shape,
                                         const kda_latent_cache* cache_shape) {
   if (check_decode(shape) != KDA_OK || check_cache(cache_shape) != KDA_OK) return 0;
-  return align_up(decode_workspace(shape->N, shape->L, shape->H), 256);
+  return align_up(decode_workspace(shape->L, shape->H), 256);
 }
 
 kda_status kda_latent_decode(const void* q, const void* cache, const int32_t* block_table,
@@ -246,7 +246,7 @@ kda_status kda_latent_decode(const void* q, const void* cache, const int32_t* bl
       (block_table == nullptr && s.table_pages > 0) ||
       (cache == nullptr && cache_shape->n_pages > 0))
     return KDA_ERR_INVALID_ARG;
-  if (s.table_pages > kMaxTokens / cache_shape->page_size) return KDA_ERR_UNSUPPORTED;
+  if (s.table_pages > (kMaxTokens - 256) / cache_shape->page_size) return KDA_ERR_UNSUPPORTED;
   if (workspace == nullptr || misaligned(workspace, 255) ||
       workspace_bytes < kda_latent_decode_workspace_size(shape, cache_shape))
     return KDA_ERR_INVALID_ARG;

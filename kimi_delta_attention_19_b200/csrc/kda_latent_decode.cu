@@ -1,93 +1,840 @@
-// kda_latent_decode.cu -- absorbed latent attention over the paged cache: one warp a row.
-#include <cuda_fp8.h>
-
-#include "kda_latent.cuh"
+// kda_latent_decode.cu -- absorbed latent attention over the paged cache.
+//
+//   s_j = scale q . x_j (576),  p = softmax_j(s),  o = sum_j p_j x_j[0:512]
+//
+// Bound by memory: a cached vector (1152 bytes, or 656 in 8 bits) is read once for all heads
+// and used for 2 x (576 + 512) operations a head. 64 cached vectors at a time are a tile X
+// [64 keys, 576], staged in shared memory once and used as the A operand of both products:
+//   S^T [64 keys, rows]   = X Q^T        (K-major A),          rows = (query token, head)
+//   O^T [512 ch, rows]   += X[:, :512]^T P^T  (MN-major A: the same bytes)
+// so up to 64 rows cost one pass over X and short products do not waste the tensor core's
+// 128 rows on 16 or 32 heads. A thread holds a key, the softmax statistics are per row (a
+// column here) and uniform over the threads. They follow the running maximum lazily: a
+// column's reference is raised only when a score passes it by 2^8 (one barrier with a vote a
+// tile; p stays below 256, sums are fp32), which for real data is a tile or two a sequence;
+// only then are O^T and the sums rescaled.
+//
+// Work: the (sequence, row block, tile) triples in order are cut into equal runs, one per SM,
+// so ragged lengths balance and one long sequence fills the GPU; the at most two units a run
+// does not cover whole leave fp32 partials, which a second kernel joins. Nothing is decided
+// on the host: lengths may change under a captured graph.
+//
+// Warps: 0 loads (TMA boxes of a page's rows, 64 channels wide; two 74 KB stages, each in
+// five groups that are loaded and released separately), 1 issues the products (whichever of
+// the next tile's S^T or this tile's O^T is ready), 4-7 softmax and results; with an 8-bit
+// cache warps 8-15 read the codes and write them as bf16 (exact) into the stage.
+#include "kda_latent_tc.cuh"
 
 namespace kda {
 namespace latent {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int KT = 64;                    // keys of a tile
+constexpr int kAtoms = DX / 64;           // 64-channel column groups of a tile
+constexpr uint32_t kAtom = KT * 128;      // bytes of one
+constexpr uint32_t kStage = kAtoms * kAtom;
+constexpr int kGroups = 5;                // column groups loaded together: 4 x 128 channels, k_pe
+constexpr int kMaxCtas = 160;             // of the workspace; the grid is at most this
+constexpr float kRaise = 8.f;             // log2 units a score may pass its column's reference
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  return x;
+template <int NC>
+struct Sm {
+  static constexpr uint32_t X = 0, Q = 2 * kStage, P = Q + kAtoms * NC * 128,
+                            BAR = P + KT * 128, TM = BAR + 28 * 8, BAIL = TM + 4, BADT = BAIL + 4,
+                            WORDS = BADT + 24, RED = WORDS + NC * 8, FAC = RED + 4 * NC * 4,
+                            START = FAC + NC * 4, BYTES = START + 64;
+};
+static_assert(Sm<64>::BYTES <= 232448, "shared memory");
+static_assert(Sm<64>::WORDS % 8 == 0 && Sm<64>::START % 8 == 0 && Sm<16>::START % 8 == 0, "");
+
+struct Rec {               // per CTA, for the joining kernel
+  int32_t cont, cont_lead, cont_last;  // unit its run begins inside of (-1: none), CTAs of it
+  int32_t lead, lead_last;             // unit it leads into the next CTA (-1: none)
+  int32_t pad[3];
+};
+struct Layout {
+  size_t ml, part, total;
+};
+__host__ __device__ inline Layout ws_layout(int nc) {
+  Layout l;
+  l.ml = kMaxCtas * sizeof(Rec);
+  l.part = l.ml + sizeof(float2) * kMaxCtas * 2 * nc;
+  l.total = l.part + sizeof(float) * kMaxCtas * 2 * nc * DC;
+  return l;
 }
 
-__device__ __forceinline__ void ld_row(const CacheArgs& c, int64_t slot, int lane, float (&x)[18]) {
-  const __nv_bfloat16* pe;
-  if (c.format == KDA_CACHE_BF16) {
-    const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(c.cache + slot * DX * 2);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = __bfloat162float(row[16 * lane + i]);
-    pe = row + DC;
-  } else {
-    const unsigned char* row = c.cache + slot * kRow8;
-    const float e = __uint_as_float(static_cast<uint32_t>(row[kExp8 + lane / 8]) << 23);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const __half_raw h = __nv_cvt_fp8_to_halfraw(row[16 * lane + i], __NV_E4M3);
-      x[i] = __half2float(__half(h)) * e;
-    }
-    pe = reinterpret_cast<const __nv_bfloat16*>(row + kPe8);
-  }
-  x[16] = __bfloat162float(pe[2 * lane]);
-  x[17] = __bfloat162float(pe[2 * lane + 1]);
+struct Args {
+  DecodeLatentArgs d;
+  int rb;                // row blocks of a sequence
+  int R;                 // rows of a sequence, L * H
+};
+struct Maps {
+  CUtensorMap x, q;
+};
+
+__device__ __forceinline__ bool len_ok(const DecodeLatentArgs& d, int64_t len) {
+  return len >= 0 && len <= d.table_pages * d.c.page_size && (len == 0 || d.c.n_pages > 0);
+}
+__device__ __forceinline__ int tiles_of(const DecodeLatentArgs& d, int64_t len) {
+  return len_ok(d, len) ? static_cast<int>((len + KT - 1) / KT) : 0;
 }
 
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(DecodeLatentArgs a) {
-  const int lane = threadIdx.x % 32, rows = a.L * a.H;
-  const int row = blockIdx.x * kWarps + threadIdx.x / 32, n = blockIdx.y;
-  if (row >= rows) return;
-  const int i = row / a.H;
-  const int64_t at = static_cast<int64_t>(n) * rows + row;
-  const int64_t len = a.lens[n];
-  __nv_bfloat16* o = a.out + at * DC + 16 * lane;
-  bool bad = len < 0 || len > a.table_pages * a.c.page_size;
-  float q[18], acc[16] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int x = 0; x < 16; ++x) q[x] = __bfloat162float(a.q[at * DX + 16 * lane + x]);
-  q[16] = __bfloat162float(a.q[at * DX + DC + 2 * lane]);
-  q[17] = __bfloat162float(a.q[at * DX + DC + 2 * lane + 1]);
-  const int64_t first = len - a.L;  // position of the first query token
-  const uint64_t word = a.mask != nullptr ? static_cast<uint64_t>(a.mask[n * a.L + i])
-                                          : (2ull << i) - 1;
-  for (int64_t j = 0; j < len && !bad; ++j) {
-    const int64_t page = a.table[n * a.table_pages + j / a.c.page_size];
-    if (page < 0 || page >= a.c.n_pages) {
-      bad = true;
-      break;
+// Walks a CTA's run: the segments (parts of units) it covers, in order.
+struct Walk {
+  int n, rb, tile;       // of the next segment
+  int left;              // tiles of the run behind it
+  int len, tiles, cnt;   // of the current segment: sequence length, unit tiles, segment tiles
+  int sn, srb, st;       // current segment: sequence, row block, first tile
+  __device__ bool next(const Args& a) {
+    if (left <= 0) return false;
+    for (;;) {
+      len = a.d.lens[n];
+      tiles = tiles_of(a.d, len);
+      if (tiles > 0) break;
+      ++n;               // the run's tiles end before N does
+      rb = tile = 0;
     }
-    if (j >= first && !(word >> (j - first) & 1)) continue;
-    float x[18], s = 0.f;
-    ld_row(a.c, page * a.c.page_size + j % a.c.page_size, lane, x);
-#pragma unroll
-    for (int k = 0; k < 18; ++k) s += q[k] * x[k];
-    s = a.scale * warp_sum(s);
-    const float m2 = fmaxf(m, s), ms = m2 == -INFINITY ? 0.f : m2;
-    const float c = __expf(m - ms), p = __expf(s - ms);
-    l = l * c + p;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) acc[k] = acc[k] * c + p * x[k];
-    m = m2;
+    sn = n;
+    srb = rb;
+    st = tile;
+    cnt = min(tiles - tile, left);
+    left -= cnt;
+    tile = 0;
+    if (++rb == a.rb) {
+      rb = 0;
+      ++n;
+    }
+    return true;
   }
-  if (bad) {
-    if (lane == 0 && a.status != nullptr) atomicExch(a.status, kDevBadPage);
-    l = NAN;
+};
+
+// four e4m3 codes as bf16 times 2^e: the code's bits in a bf16's place read as its value times
+// 2^-120, so two exact products (2^120, then 2^e in both halves of `sc`) give the value
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint2 values4(uint32_t w, uint32_t sc) {
+  uint32_t lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);  // codes in upper bytes
+  lo = (lo & 0x80008000u) | (lo >> 4 & 0x07f007f0u);
+  hi = (hi & 0x80008000u) | (hi >> 4 & 0x07f007f0u);
+  uint2 r = make_uint2(mul2(mul2(lo, 0x7b807b80u), sc), mul2(mul2(hi, 0x7b807b80u), sc));
+  if (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // a NaN among them
+    if ((w & 0x7fu) == 0x7fu) r.x |= 0x7fffu;
+    if ((w & 0x7f00u) == 0x7f00u) r.x |= 0x7fff0000u;
+    if ((w & 0x7f0000u) == 0x7f0000u) r.y |= 0x7fffu;
+    if ((w & 0x7f000000u) == 0x7f000000u) r.y |= 0x7fff0000u;
   }
+  return r;
+}
+
+template <int NC, bool F8>
+__global__ void __launch_bounds__(F8 ? 512 : 256, 1)
+    decode_kernel(const __grid_constant__ Maps maps, const Args a) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  using S = Sm<NC>;
+  constexpr int NH = NC / 2;                     // rows a softmax thread holds
+  constexpr uint32_t kCols = NC == 64 ? 512 : NC == 32 ? 256 : 128;  // 4 NC of O^T, 2 NC of S^T
+  constexpr int kThreads = F8 ? 512 : 256;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR);
+  uint64_t *full = bar, *empty = bar + 10, *s_full = bar + 20, *p_full = bar + 22,
+           *pv_done = bar + 23, *q_full = bar + 24, *q_empty = bar + 25, *o_free = bar + 26,
+           *drain = bar + 27;
+  uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + S::TM);
+  volatile int* bail = reinterpret_cast<volatile int*>(sm + S::BAIL);
+  volatile int* bad_tile = reinterpret_cast<volatile int*>(sm + S::BADT);
+  uint64_t* words = reinterpret_cast<uint64_t*>(sm + S::WORDS);
+  float* red = reinterpret_cast<float*>(sm + S::RED);
+  float* fac = reinterpret_cast<float*>(sm + S::FAC);
+  int64_t* start = reinterpret_cast<int64_t*>(sm + S::START);
+  const uint32_t sb = smem_u32(sm);
+  const DecodeLatentArgs& d = a.d;
+  Rec* rec = reinterpret_cast<Rec*>(d.ws) + blockIdx.x;
+  const Layout wl = ws_layout(NC);
+
+  if (sb & 1023) {  // the operand tiles need it, and nothing else is in shared memory
+    if (tid == 0 && d.status != nullptr) atomicExch(d.status, kDevWaitTimeout);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 10; ++i) {
+      mbar_init(full + i, F8 ? 8 : 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_full + 1, 1);
+    mbar_init(p_full, 128);
+    mbar_init(pv_done, 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(o_free, 128);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *bail = 0;
+    bad_tile[0] = bad_tile[1] = 0;
+    rec->cont = rec->lead = -1;
+    tma_prefetch_desc(&maps.q);
+    if (!F8) tma_prefetch_desc(&maps.x);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem, kCols);
+    tmem_relinquish();
+  }
+  // This CTA's run: tiles [t0, t1) of all sequences' tiles in order.
+  const int per = (d.N + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int n = tid * per; n < min(d.N, (tid + 1) * per); ++n)
+    mine += static_cast<int64_t>(tiles_of(d, d.lens[n])) * a.rb;
+  int64_t pre = mine;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) st_out(o + k, bad ? NAN : l == 0.f ? 0.f : acc[k] / l);
-  if (lane == 0 && a.lse != nullptr) a.lse[at] = bad ? NAN : l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + logf(l);
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, pre, off);
+    if (lane >= off) pre += up;
+  }
+  int64_t* wsum = reinterpret_cast<int64_t*>(sm + S::P);  // not in use yet
+  if (lane == 31) wsum[warp] = pre;
+  __syncthreads();
+  int64_t total = 0;
+  pre -= mine;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) pre += wsum[w];
+    total += wsum[w];
+  }
+  const int64_t G = total < gridDim.x ? total : gridDim.x;
+  const int64_t c = blockIdx.x;
+  const int64_t t0 = c < G ? c * total / G : 0, t1 = c < G ? (c + 1) * total / G : 0;
+  if (t0 < t1 && pre <= t0 && t0 < pre + mine) {
+    int64_t at = pre;
+    for (int n = tid * per;; ++n) {
+      const int tl = tiles_of(d, d.lens[n]);
+      const int64_t u = static_cast<int64_t>(tl) * a.rb;
+      if (t0 < at + u) {
+        start[0] = n;
+        start[1] = (t0 - at) / tl;
+        start[2] = (t0 - at) % tl;
+        break;
+      }
+      at += u;
+    }
+  }
+  // sequences without a tile: empty (zeros) or refused (NaN), spread over the CTAs
+  for (int n = blockIdx.x; n < d.N; n += gridDim.x) {
+    const int64_t len = d.lens[n];
+    if (tiles_of(d, len) > 0) continue;
+    const bool bad = !len_ok(d, len);
+    if (bad && tid == 0 && d.status != nullptr) atomicExch(d.status, kDevBadPage);
+    const uint4 v = bad ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu)
+                        : make_uint4(0, 0, 0, 0);
+    uint4* o = reinterpret_cast<uint4*>(d.out + static_cast<int64_t>(n) * a.R * DC);
+    for (int64_t i = tid; i < static_cast<int64_t>(a.R) * (DC / 8); i += kThreads) o[i] = v;
+    if (d.lse != nullptr)
+      for (int i = tid; i < a.R; i += kThreads)
+        d.lse[static_cast<int64_t>(n) * a.R + i] = bad ? NAN : -INFINITY;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();  // the joining kernel waits for this one's end by itself
+  const uint32_t tb = *tmem;
+  Walk wk;
+  wk.left = static_cast<int>(t1 - t0);
+  wk.n = wk.left > 0 ? static_cast<int>(start[0]) : 0;
+  wk.rb = wk.left > 0 ? static_cast<int>(start[1]) : 0;
+  wk.tile = wk.left > 0 ? static_cast<int>(start[2]) : 0;
+  const int n_tiles = wk.left;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ loads
+    const int ps = d.c.page_size, pr = ps < KT ? ps : KT;  // rows of a box
+    int t = 0, q_loads = 0;
+    for (int seg = 0; wk.next(a); ++seg) {
+      auto load_q = [&] {
+        if (seg > 0) wait_for(q_empty, (seg - 1) & 1, bail);
+        if (bailed(bail)) return;
+        ++q_loads;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, kAtoms * NC * 128);
+        __syncwarp();
+        if (lane < kAtoms)
+          tma_load_2d(sm + S::Q + lane * NC * 128, &maps.q, q_full, lane * 64,
+                      wk.sn * a.R + wk.srb * NC);
+      };
+      if (F8 || seg == 0) load_q();
+      for (int i = 0; !F8 && i < wk.cnt; ++i, ++t) {
+        const int s = t & 1;
+        const int pos = (wk.st + i) * KT + lane * pr;
+        int64_t page = 0;
+        const bool there = lane < KT / pr && pos < wk.len;
+        if (there) page = d.table[wk.sn * d.table_pages + pos / ps];
+        const bool bad = page < 0 || page >= d.c.n_pages;
+        if (bad) page = 0;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) bad_tile[s] = t + 1;
+        const int nb = __popc(__ballot_sync(0xffffffffu, there));
+        const int row = static_cast<int>(page * ps + pos % ps);
+        const int y = __shfl_sync(0xffffffffu, row, lane >> 1 & 3);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
+          if (bailed(bail)) continue;
+          uint64_t* f = full + s * kGroups + g;
+          if (lane == 0) mbar_arrive_expect_tx(f, nb * pr * (g < 4 ? 256 : 128));
+          __syncwarp();
+          const int atom = 2 * g + (lane & 1);
+          if (lane < 2 * nb && atom < kAtoms)
+            tma_load_2d(sm + S::X + s * kStage + atom * kAtom + (lane >> 1) * pr * 128, &maps.x, f,
+                        atom * 64, y);
+        }
+        if (seg > 0 && i == 0) load_q();
+      }
+    }
+    if (bailed(bail)) {  // let the copies in flight land before the CTA ends
+      if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, 20000000LL);
+      for (int k = t > 2 ? t - 2 : 0; k < t; ++k)
+        for (int g = 0; g < kGroups; ++g)
+          mbar_wait(full + (k & 1) * kGroups + g, k / 2 & 1, 20000000LL);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- products
+    constexpr uint32_t iq = idesc_bf16(64, NC, 0, 0), ip = idesc_bf16(128, NC, 1, 1);
+    Walk wp = wk;  // the segment of the next O^T product; wk: of the next S^T product
+    int qt = 0, qg = 0, qi = 0, qs = -1, pt = 0, pi = 0, pseg = -1;
+    wk.cnt = wp.cnt = 0;
+    long long last = clock64();
+    while (pt < n_tiles) {
+      bool moved = false;
+      const bool dead = bailed(bail);
+      if (qt < n_tiles && qt <= pt + 1) {  // next column group of S^T
+        if (qg == 0 && qi == wk.cnt) {     // a new segment
+          wk.next(a);
+          qi = 0;
+          ++qs;
+        }
+        const int s = qt & 1;
+        const bool ready = mbar_test(full + s * kGroups + qg, qt / 2 & 1) &&
+                           (qg > 0 || qi > 0 || mbar_test(q_full, qs & 1));
+        if (__all_sync(0xffffffffu, ready) || dead) {
+          moved = true;
+          tc_fence_after();
+          if (elect_one() && !dead) {
+            const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage + 2 * qg * kAtom, 16, 1024);
+            const uint64_t qb = sdesc_sw128(sb + S::Q + 2 * qg * NC * 128, 16, 1024);
+            const uint32_t dst = tb + 4 * NC + s * NC;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(dst, xa + 2 * k, qb + 2 * k, iq, qg > 0 || k > 0);
+            if (qg < 4) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_bf16(dst, xa + kAtom / 16 + 2 * k, qb + NC * 8 + 2 * k, iq, 1);
+            } else {
+              umma_commit(s_full + s);
+              umma_commit(empty + s * kGroups + 4);
+              if (qi + 1 == wk.cnt) umma_commit(q_empty);
+            }
+          }
+          __syncwarp();
+          if (++qg == kGroups) {
+            qg = 0;
+            ++qi;
+            ++qt;
+          }
+        }
+      }
+      if (pt < qt) {  // O^T of the tile whose P is ready
+        const bool first = pi == wp.cnt;
+        const bool ready = mbar_test(p_full, pt & 1) &&
+                           (!first || pseg < 0 || mbar_test(o_free, pseg & 1));
+        if (__all_sync(0xffffffffu, ready) || dead) {
+          moved = true;
+          if (first) {
+            wp.next(a);
+            pi = 0;
+            ++pseg;
+          }
+          tc_fence_after();
+          if (elect_one() && !dead) {
+            const int s = pt & 1;
+            const uint64_t pb = sdesc_sw128(sb + S::P, 8192, 1024);
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb) {
+              const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage + 2 * mb * kAtom, kAtom, 1024);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_bf16(tb + mb * NC, xa + 128 * k, pb + 128 * k, ip, pi > 0 || k > 0);
+              umma_commit(empty + s * kGroups + mb);
+            }
+            umma_commit(pv_done);
+          }
+          __syncwarp();
+          ++pi;
+          ++pt;
+        }
+      }
+      if (moved) {
+        last = clock64();
+      } else if (clock64() - last > kWaitCycles) {
+        *bail = 1;
+      }
+    }
+    if (bailed(bail)) {
+      if (elect_one()) umma_commit(drain);
+      __syncwarp();
+      mbar_wait(drain, 0, 20000000LL);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------- softmax and results
+    const int w = warp - 4, tw = tid - 128;
+    const uint32_t lanes = tb + (static_cast<uint32_t>(w * 32) << 16);
+    const int half = lane >> 4, ch0 = half * NH, kk = w * 16 + (lane & 15);
+    const float sl = d.scale * kLog2e;
+    int t = 0;
+    bool first_seg = true;
+    int64_t gt = t0;  // global index of the segment's first tile
+    for (; wk.next(a); first_seg = false) {
+      const int first = wk.len - d.L;  // position of the first query token
+      if (tw < NC) {
+        const int row = wk.srb * NC + tw, i = row / d.H;
+        words[tw] = row >= a.R ? 0
+                    : d.mask != nullptr
+                        ? static_cast<uint64_t>(d.mask[static_cast<int64_t>(wk.sn) * d.L + i])
+                        : (2ull << i) - 1;
+      }
+      group_sync(1, 128);
+      float m[NH], l[NH];
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+      bool bad = false;
+      for (int i = 0; i < wk.cnt; ++i, ++t) {
+        const int s = t & 1, valid = wk.len - (wk.st + i) * KT;
+        wait_for(s_full + s, t / 2 & 1, bail);
+        tc_fence_after();
+        bad |= bad_tile[s] == t + 1;
+        float x[NH];
+        {
+          // an M = 64 product's row r is in tensor-memory lane 32 (r / 16) + r % 16: the
+          // upper half of a warp takes the upper half of the columns from the lower one
+          const uint32_t sc = lanes + 4 * NC + s * NC;
+          if constexpr (NC == 64) {
+            uint32_t lo[32], hi[32];
+            tmem_ld32(sc, lo);
+            tmem_ld32(sc + 32, hi);
+            tmem_ld_wait(lo);
+            tmem_ld_wait(hi);
+#pragma unroll
+            for (int k = 0; k < NH; ++k) {
+              const uint32_t up = __shfl_up_sync(0xffffffffu, hi[k], 16);
+              x[k] = sl * __uint_as_float(half ? up : lo[k]);
+            }
+          } else if constexpr (NC == 32) {
+            uint32_t v[32];
+            tmem_ld32(sc, v);
+            tmem_ld_wait(v);
+#pragma unroll
+            for (int k = 0; k < NH; ++k) {
+              const uint32_t up = __shfl_up_sync(0xffffffffu, v[k + NH], 16);
+              x[k] = sl * __uint_as_float(half ? up : v[k]);
+            }
+          } else {
+            uint32_t v[16];
+            tmem_ld16(sc, v);
+            tmem_ld_wait(v);
+#pragma unroll
+            for (int k = 0; k < NH; ++k) {
+              const uint32_t up = __shfl_up_sync(0xffffffffu, v[k + NH], 16);
+              x[k] = sl * __uint_as_float(half ? up : v[k]);
+            }
+          }
+        }
+        const int kj = (wk.st + i) * KT + kk - first;  // among the query tokens
+        if (kk >= valid) {
+#pragma unroll
+          for (int k = 0; k < NH; ++k) x[k] = -INFINITY;
+        } else if (kj >= 0) {
+#pragma unroll
+          for (int k = 0; k < NH; ++k)
+            if (!(words[ch0 + k] >> kj & 1)) x[k] = -INFINITY;
+        }
+        bool up = false;
+#pragma unroll
+        for (int k = 0; k < NH; ++k) up |= x[k] > m[k] + kRaise;
+        if (group_any(1, 128, up)) {
+          // raise the columns' references to the running maximum, rescale sums and O^T
+#pragma unroll
+          for (int k = 0; k < NH; ++k) {
+            float y = x[k];
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1)
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+            if ((lane & 15) == 0) red[w * NC + ch0 + k] = y;
+          }
+          group_sync(1, 128);
+#pragma unroll
+          for (int k = 0; k < NH; ++k) {
+            const int cc = ch0 + k;
+            const float y = fmaxf(fmaxf(red[cc], red[NC + cc]), fmaxf(red[2 * NC + cc], red[3 * NC + cc]));
+            const float mn = fmaxf(m[k], y);
+            const float f = m[k] == -INFINITY ? 0.f : ex2(m[k] - mn);
+            l[k] *= f;
+            m[k] = mn;
+            if (w == 0 && (lane & 15) == 0) fac[cc] = f;
+          }
+          group_sync(1, 128);
+          if (i > 0) {
+            wait_for(pv_done, (t - 1) & 1, bail);
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 4 * NC / 16; ++q) {
+              uint32_t v[16];
+              tmem_ld16(lanes + q * 16, v);
+              tmem_ld_wait(v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                v[k] = __float_as_uint(__uint_as_float(v[k]) * fac[q * 16 % NC + k]);
+              tmem_st16(lanes + q * 16, v);
+            }
+            tmem_st_wait();
+          }
+        }
+        // p enters the product as bf16 (half a step, 2^-9 of it); its sum is kept in fp32
+        uint32_t p[NH / 2];
+#pragma unroll
+        for (int k = 0; k < NH; k += 2) {
+          const float a0 = ex2(x[k] - (m[k] == -INFINITY ? 0.f : m[k]));
+          const float a1 = ex2(x[k + 1] - (m[k + 1] == -INFINITY ? 0.f : m[k + 1]));
+          l[k] += a0;
+          l[k + 1] += a1;
+          p[k / 2] = pack2(a0, a1);
+        }
+        if (t > 0) wait_for(pv_done, (t - 1) & 1, bail);  // P is free
+#pragma unroll
+        for (int q = 0; q < NH / 8; ++q)
+          *reinterpret_cast<uint4*>(sm + S::P + sw128_chunk(kk, ch0 / 8 + q, 0)) =
+              make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+        if (!F8 && valid < KT) {  // rows past the sequence may hold anything: 0 x NaN is NaN
+          for (int e = tw; e < (KT - valid) * 64; e += 128) {
+            const int r = valid + (e >> 6), ck = e & 63;
+            *reinterpret_cast<uint4*>(sm + S::X + s * kStage + sw128_chunk(r, ck, kAtom)) =
+                make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full);
+      }
+      // the segment's sums
+      group_sync(1, 128);  // the last tile's factors are read
+#pragma unroll
+      for (int k = 0; k < NH; ++k) {
+        float y = l[k];
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+        if ((lane & 15) == 0) {
+          red[w * NC + ch0 + k] = y;
+          if (w == 0) fac[ch0 + k] = m[k];
+        }
+      }
+      group_sync(1, 128);
+      const bool whole = wk.st == 0 && wk.cnt == wk.tiles;
+      const int slot = wk.st > 0 ? 0 : 1;
+      const int64_t part = (c * 2 + slot) * NC;
+      const int64_t row0 = static_cast<int64_t>(wk.sn) * a.R + wk.srb * NC;
+      const int rows = min(NC, a.R - wk.srb * NC);
+      float mul = 1.f;
+      if (tw < NC) {
+        const float ls = (red[tw] + red[NC + tw]) + (red[2 * NC + tw] + red[3 * NC + tw]);
+        const float ms = fac[tw];
+        if (whole) {
+          mul = bad ? NAN : ls == 0.f ? 0.f : 1.f / ls;
+          if (tw < rows && d.lse != nullptr)
+            d.lse[row0 + tw] = bad ? NAN : ls == 0.f ? -INFINITY : (ms + log2f(ls)) * kLn2;
+        } else {
+          reinterpret_cast<float2*>(d.ws + wl.ml)[part + tw] = make_float2(ms, bad ? NAN : ls);
+        }
+      }
+      group_sync(1, 128);
+      if (tw < NC) fac[tw] = mul;
+      if (tw == 0) {
+        if (bad && d.status != nullptr) atomicExch(d.status, kDevBadPage);
+        if (*bail && d.status != nullptr) atomicExch(d.status, kDevWaitTimeout);
+        const int64_t u0 = gt - wk.st, u1 = u0 + wk.tiles - 1;  // the unit's first, last tile
+        const int unit = wk.sn * a.rb + wk.srb;
+        const int last_cta = static_cast<int>(((u1 + 1) * G - 1) / total);
+        if (wk.st > 0) {
+          rec->cont_lead = static_cast<int>(((u0 + 1) * G - 1) / total);
+          rec->cont_last = last_cta;
+          rec->cont = unit;
+        } else if (!whole) {
+          rec->lead_last = last_cta;
+          rec->lead = unit;
+        }
+      }
+      group_sync(1, 128);
+      wait_for(pv_done, (t - 1) & 1, bail);
+      tc_fence_after();
+#pragma unroll 1
+      for (int q = 0; q < 4 * NC / 16; ++q) {
+        uint32_t v[16];
+        tmem_ld16(lanes + q * 16, v);
+        tmem_ld_wait(v);
+        const int c0 = q * 16 % NC, ch = q * 16 / NC * 128 + w * 32 + lane;
+        if (whole) {
+          // lane pairs trade values, so that each writes two adjacent channels of a row
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const float f0 = __uint_as_float(v[k]) * fac[c0 + k];
+            const float f1 = __uint_as_float(v[k + 1]) * fac[c0 + k + 1];
+            const float o = __shfl_xor_sync(0xffffffffu, lane & 1 ? f0 : f1, 1);
+            const int r = c0 + k + (lane & 1);
+            const uint32_t pk = lane & 1 ? pack2(o, f1) : pack2(f0, o);
+            if (r < rows)
+              *reinterpret_cast<uint32_t*>(d.out + (row0 + r) * DC + (ch & ~1)) = pk;
+          }
+        } else {
+          float* dst = reinterpret_cast<float*>(d.ws + wl.part) + (part + c0) * DC + ch;
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (c0 + k < rows) dst[k * DC] = __uint_as_float(v[k]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(o_free);
+      gt += wk.cnt;
+      group_sync(1, 128);  // fac, red and words are free
+    }
+  } else if (F8 && warp >= 8) {
+    // ------------------------------------------- 8-bit rows, as bf16 into the stages
+    // Thread (row, quarter): 32 codes of each 128-channel group. A group's registers are
+    // refilled with the next tile's codes as soon as they are converted, so ~40 KB an SM are
+    // in flight; the block table is read a tile further ahead.
+    const int i = tid - 256, row = i / 4, qd = i % 4;
+    Walk wl2 = wk;   // runs ahead
+    int li = 0;
+    wl2.cnt = 0;
+    int ahead = 0;
+    struct Row {
+      const unsigned char* p;  // null: no row there
+      bool bad;
+    };
+    auto fetch = [&]() -> Row {
+      if (ahead >= n_tiles) return Row{nullptr, false};
+      ++ahead;
+      if (li == wl2.cnt) {
+        wl2.next(a);
+        li = 0;
+      }
+      const int pos = (wl2.st + li++) * KT + row;
+      if (pos >= wl2.len) return Row{nullptr, false};
+      const int64_t page = d.table[wl2.sn * d.table_pages + pos / d.c.page_size];
+      if (page < 0 || page >= d.c.n_pages) return Row{nullptr, true};
+      return Row{d.c.cache + (page * d.c.page_size + pos % d.c.page_size) * kRow8, false};
+    };
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto ld = [&](const Row& r, int off) {
+      return r.p != nullptr ? __ldg(reinterpret_cast<const uint4*>(r.p + off)) : zero;
+    };
+    uint4 code[4][2], pe[2];
+    uint32_t ex = 0;
+    Row cur = fetch(), nxt = fetch();
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) code[g][h] = ld(cur, g * 128 + qd * 32 + h * 16);
+    pe[0] = ld(cur, kPe8 + qd * 32);
+    pe[1] = ld(cur, kPe8 + qd * 32 + 16);
+    ex = cur.p != nullptr ? *reinterpret_cast<const uint32_t*>(cur.p + kExp8) : 0;
+    for (int t = 0; t < n_tiles; ++t) {
+      const int s = t & 1;
+      const Row nn = fetch();
+      unsigned char* xs = sm + S::X + s * kStage;
+      if (cur.bad) bad_tile[s] = t + 1;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t e = ex >> (8 * g) & 0xffu, scale = e << 7 | e << 23;
+        uint32_t v[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t wd[4] = {code[g][h].x, code[g][h].y, code[g][h].z, code[g][h].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint2 r = values4(wd[k], scale);
+            v[8 * h + 2 * k] = r.x;
+            v[8 * h + 2 * k + 1] = r.y;
+          }
+          code[g][h] = ld(nxt, g * 128 + qd * 32 + h * 16);
+        }
+        if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
+        // the chunk order differs by thread, so that 8 threads' stores touch all banks
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int jj = j ^ (qd >> 1) ^ ((row & 1) << 1);
+          uint4 o;
+          o.x = jj & 2 ? (jj & 1 ? v[12] : v[8]) : (jj & 1 ? v[4] : v[0]);
+          o.y = jj & 2 ? (jj & 1 ? v[13] : v[9]) : (jj & 1 ? v[5] : v[1]);
+          o.z = jj & 2 ? (jj & 1 ? v[14] : v[10]) : (jj & 1 ? v[6] : v[2]);
+          o.w = jj & 2 ? (jj & 1 ? v[15] : v[11]) : (jj & 1 ? v[7] : v[3]);
+          *reinterpret_cast<uint4*>(xs + sw128_chunk(row, g * 16 + qd * 4 + jj, kAtom)) = o;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + s * kGroups + g);
+      }
+      if (t >= 2) wait_for(empty + s * kGroups + 4, (t / 2 - 1) & 1, bail);
+      *reinterpret_cast<uint4*>(xs + sw128_chunk(row, 64 + qd * 2, kAtom)) = pe[0];
+      *reinterpret_cast<uint4*>(xs + sw128_chunk(row, 64 + qd * 2 + 1, kAtom)) = pe[1];
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + s * kGroups + 4);
+      pe[0] = ld(nxt, kPe8 + qd * 32);
+      pe[1] = ld(nxt, kPe8 + qd * 32 + 16);
+      ex = nxt.p != nullptr ? *reinterpret_cast<const uint32_t*>(nxt.p + kExp8) : 0;
+      cur = nxt;
+      nxt = nn;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tb, kCols);
+  }
+}
+
+// Joins the partials of the units that runs cut: sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
+// over the CTAs of a unit, in their order. Four rows a block (128 threads each, 4 channels a
+// thread); a unit of more than 8 CTAs gives every row a block of its own (the blocks of the
+// CTAs in between help), whose four groups each take a quarter of the partials.
+template <int NC>
+__global__ void __launch_bounds__(512) join_kernel(const Args a) {
+  griddep_wait();
+  const Rec r = reinterpret_cast<const Rec*>(a.d.ws)[blockIdx.x];
+  const Layout wl = ws_layout(NC);
+  const float2* ml = reinterpret_cast<const float2*>(a.d.ws + wl.ml);
+  const float* part = reinterpret_cast<const float*>(a.d.ws + wl.part);
+  __shared__ float4 acc_s[4][128];
+  __shared__ float ml_s[4][2];
+  const int grp = threadIdx.x / 128, th = threadIdx.x % 128;
+  for (int pass = 0; pass < 2; ++pass) {
+    const int unit = pass ? r.cont : r.lead;
+    if (unit < 0) continue;
+    const int c0 = pass ? r.cont_lead : blockIdx.x, c1 = pass ? r.cont_last : r.lead_last;
+    const bool wide = c1 - c0 + 1 > 8;
+    if (!wide && pass) continue;
+    const int k = wide ? (blockIdx.x - c0) * gridDim.y + blockIdx.y : 0;
+    const int row = wide ? k : blockIdx.y * 4 + grp;
+    const int n = unit / a.rb, rb = unit % a.rb, rows = min(NC, a.R - rb * NC);
+    if (wide && row >= rows) continue;
+    const int np = c1 - c0 + 1;
+    const int p0 = wide ? np * grp / 4 : 0, p1 = wide ? np * (grp + 1) / 4 : row < rows ? np : 0;
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto at = [&](int p) { return ((c0 + p) * 2 + (p == 0 ? 1 : 0)) * NC + row; };
+    for (int p = p0; p < p1; ++p) M = fmaxf(M, ml[at(p)].x);
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) {
+      const float2 x = ml[at(p)];
+      const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
+      const float4 o = __ldcs(reinterpret_cast<const float4*>(part + static_cast<int64_t>(at(p)) * DC) + th);
+      l += x.y != x.y ? x.y : f * x.y;  // NaN: a page out of range
+      acc.x += f * o.x;
+      acc.y += f * o.y;
+      acc.z += f * o.z;
+      acc.w += f * o.w;
+    }
+    if (wide) {
+      acc_s[grp][th] = acc;
+      if (th == 0) {
+        ml_s[grp][0] = M;
+        ml_s[grp][1] = l;
+      }
+      __syncthreads();
+      M = fmaxf(fmaxf(ml_s[0][0], ml_s[1][0]), fmaxf(ml_s[2][0], ml_s[3][0]));
+      l = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int g = 0; g < 4; ++g) {
+        const float f = ml_s[g][0] == -INFINITY ? 0.f : exp2f(ml_s[g][0] - M);
+        const float gl = ml_s[g][1];
+        l += gl != gl ? gl : f * gl;
+        const float4 o = acc_s[g][th];
+        acc.x += f * o.x;
+        acc.y += f * o.y;
+        acc.z += f * o.z;
+        acc.w += f * o.w;
+      }
+      __syncthreads();
+      if (grp != 0) continue;
+    } else if (row >= rows) {
+      continue;
+    }
+    const float mul = l == 0.f ? 0.f : 1.f / l;
+    const int64_t o = static_cast<int64_t>(n) * a.R + rb * NC + row;
+    const bool nan = l != l;  // poisons rows whose partials were not
+    *reinterpret_cast<uint2*>(a.d.out + o * DC + 4 * th) =
+        nan ? make_uint2(0x7fff7fffu, 0x7fff7fffu)
+            : make_uint2(pack2(acc.x * mul, acc.y * mul), pack2(acc.z * mul, acc.w * mul));
+    if (th == 0 && a.d.lse != nullptr)
+      a.d.lse[o] = nan ? l : l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+  }
+}
+
+// Rows of a block: the fewest of 16, 32, 64 that hold a sequence's rows, else 64 (more rows
+// would not fit the query block beside two stages; 16 and 32 leave the tensor pipe half idle).
+int block_rows(int L, int H) {
+  const int64_t r = static_cast<int64_t>(L) * H;
+  return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+}
+
+template <int NC, bool F8>
+cudaError_t launch(const DecodeLatentArgs& d, cudaStream_t st) {
+  Args a{d, (d.L * d.H + NC - 1) / NC, d.L * d.H};
+  Maps m;
+  memset(&m, 0, sizeof m);
+  const int64_t rows = d.c.n_pages * d.c.page_size;
+  {
+    const uint64_t dims[2] = {DX, static_cast<uint64_t>(d.N) * a.R}, strides[1] = {DX * 2};
+    const uint32_t box[2] = {64, NC};
+    if (!make_tensor_map(&m.q, d.q, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  if (!F8 && rows > 0) {
+    const uint64_t dims[2] = {DX, static_cast<uint64_t>(rows)}, strides[1] = {DX * 2};
+    const uint32_t box[2] = {64, static_cast<uint32_t>(d.c.page_size < KT ? d.c.page_size : KT)};
+    if (!make_tensor_map(&m.x, d.c.cache, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  auto kern = decode_kernel<NC, F8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Sm<NC>::BYTES);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  kern<<<grid, F8 ? 512 : 256, Sm<NC>::BYTES, st>>>(m, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, NC / 4);
+  cfg.blockDim = dim3(512);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<NC>, a);
 }
 
 }  // namespace
 
-size_t decode_workspace(int N, int L, int H) { return 256; }
+size_t decode_workspace(int L, int H) { return ws_layout(block_rows(L, H)).total; }
 
-cudaError_t launch_latent_decode(const DecodeLatentArgs& a, cudaStream_t st) {
-  decode_kernel<<<dim3((a.L * a.H + kWarps - 1) / kWarps, a.N), kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_latent_decode(const DecodeLatentArgs& d, cudaStream_t st) {
+  const bool f8 = d.c.format == KDA_CACHE_E4M3;
+  switch (block_rows(d.L, d.H)) {
+    case 16: return f8 ? launch<16, true>(d, st) : launch<16, false>(d, st);
+    case 32: return f8 ? launch<32, true>(d, st) : launch<32, false>(d, st);
+    default: return f8 ? launch<64, true>(d, st) : launch<64, false>(d, st);
+  }
 }
 
 }  // namespace latent

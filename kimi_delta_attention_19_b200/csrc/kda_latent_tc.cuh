@@ -1,0 +1,81 @@
+// kda_latent_tc.cuh -- what the latent-attention tensor-core kernels share: bounded waits,
+// the election of an issuing thread, conversions, tensor maps. Not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+
+#include "kda_latent.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace latent {
+
+using namespace sm100;
+
+// One thread of a converged warp, the same one each time. A branch on it is known to be
+// uniform, so tcgen05.mma issues every ~25 clocks; under `lane == 0` each one took ~97
+// (measured, M = 128, N = 32, 512 in a row): more than the instruction itself.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// Bounded waits. `bail` is a shared word of the CTA: the first wait that runs out (about a
+// second) sets it, every later wait returns at once, no further copy or product is issued,
+// and all loops run to their ends (so no named barrier is left short); the kernel then waits
+// for what it has in flight, reports kDevWaitTimeout and frees its tensor memory.
+constexpr long long kWaitCycles = 2000000000LL;
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* bail) {
+  if (mbar_try_wait(bar, parity)) return;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*bail) return;
+    if (clock64() - t0 > kWaitCycles) {
+      *bail = 1;
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ bool bailed(volatile int* bail) {  // the same answer for a whole warp
+  return __any_sync(0xffffffffu, *bail != 0);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two values as bf16 (round to nearest even), `lo` in the lower half
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Tiled bf16 tensor map of `rank` dimensions (the innermost one contiguous, strides in bytes
+// of the others), whose boxes land in the 128-byte-swizzled operand layout.
+bool make_tensor_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box);
+
+// The device's SM count (148 on B200): the width of the persistent grids.
+int sm_count();
+
+}  // namespace latent
+}  // namespace kda
