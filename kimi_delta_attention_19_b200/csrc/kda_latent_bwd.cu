@@ -1,4 +1,4 @@
-// kda_latent_attn.cu -- expanded latent attention, forward and backward: one warp a row.
+// kda_latent_bwd.cu -- expanded latent attention, backward: one warp a row.
 #include "kda_latent.cuh"
 
 namespace kda {
@@ -30,37 +30,6 @@ __device__ __forceinline__ float dot4(const float (&a)[4], const float (&b)[4]) 
 // First key query i does not see.
 __device__ __forceinline__ int key_end(const AttnArgs& a, const SeqRange& r, int i) {
   return a.causal ? max(0, min(r.lk, i + 1 + r.lk - r.lq)) : r.lk;
-}
-
-__global__ void __launch_bounds__(kWarps * 32) fwd_kernel(AttnArgs a) {
-  const int lane = threadIdx.x % 32, h = blockIdx.y;
-  SeqRange r;
-  if (!seq_range(a, blockIdx.z, r)) return;
-  const int i = blockIdx.x * kWarps + threadIdx.x / 32;
-  if (i >= r.lq) return;
-  const int64_t t = r.q0 + i;
-  float qn[4], qp[2], acc[4] = {0.f, 0.f, 0.f, 0.f};
-  ld4(a.q + t * a.qt + h * a.qh + 4 * lane, qn);
-  ld2(a.q + t * a.qt + h * a.qh + DN + 2 * lane, qp);
-  float m = -INFINITY, l = 0.f;
-  const int end = key_end(a, r, i);
-  for (int j = 0; j < end; ++j) {
-    float kn[4], kp[2], v[4];
-    ld4(a.kn + (r.k0 + j) * a.kt + h * a.kh + 4 * lane, kn);
-    ld2(a.kp + (r.k0 + j) * a.pt + 2 * lane, kp);
-    ld4(a.v + (r.k0 + j) * a.vt + h * a.vh + 4 * lane, v);
-    const float s = a.scale * warp_sum(dot4(qn, kn) + qp[0] * kp[0] + qp[1] * kp[1]);
-    const float m2 = fmaxf(m, s), ms = m2 == -INFINITY ? 0.f : m2;
-    const float c = __expf(m - ms), p = __expf(s - ms);
-    l = l * c + p;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) acc[x] = acc[x] * c + p * v[x];
-    m = m2;
-  }
-  __nv_bfloat16* o = a.out + (t * a.H + h) * DV + 4 * lane;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) st_out(o + x, l == 0.f ? 0.f : acc[x] / l);
-  if (lane == 0 && a.lse != nullptr) a.lse[t * a.H + h] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + logf(l);
 }
 
 __global__ void __launch_bounds__(kWarps * 32) dq_kernel(AttnArgs a) {
@@ -148,11 +117,6 @@ __global__ void dpe_kernel(AttnArgs a, int64_t tk_total) {
 unsigned blocks(int64_t n, int per) { return static_cast<unsigned>((n + per - 1) / per); }
 
 }  // namespace
-
-cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
-  fwd_kernel<<<dim3(blocks(a.max_q, kWarps), a.H, a.n_seqs), kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t st) {
   const int64_t tk_total = a.cu_k != nullptr ? a.Tk : a.Tk * a.n_seqs;

@@ -29,6 +29,16 @@ bool make_tensor_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* 
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_head_map(CUtensorMap* m, const void* ptr, int channels, int64_t heads, int64_t head,
+                   int64_t rows, int64_t token, uint32_t box_rows) {
+  if (rows < 1) return true;
+  const uint64_t dims[3] = {static_cast<uint64_t>(channels), static_cast<uint64_t>(heads),
+                            static_cast<uint64_t>(rows)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(head) * 2, static_cast<uint64_t>(token) * 2};
+  const uint32_t box[3] = {64, 1, box_rows};
+  return make_tensor_map(m, ptr, 3, dims, strides, box);
+}
+
 int sm_count() {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess)

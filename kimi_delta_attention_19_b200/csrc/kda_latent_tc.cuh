@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <string.h>
 
 #include "kda_latent.cuh"
 #include "kda_sm100.cuh"
@@ -67,12 +68,64 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// pairs of fp32 values, one instruction for both
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r, x, y, z;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  memcpy(&z, &c, 8);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  float2 o;
+  memcpy(&o, &r, 8);
+  return o;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r, x, y;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  memcpy(&o, &r, 8);
+  return o;
+}
+__device__ __forceinline__ float2 mul2f(float2 a, float2 b) {
+  unsigned long long r, x, y;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  memcpy(&o, &r, 8);
+  return o;
+}
+// 3-D tiled bulk copy global -> shared (x innermost, x * sizeof(elem) 16-byte aligned)
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int x,
+                                            int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Tiled bf16 tensor map of `rank` dimensions (the innermost one contiguous, strides in bytes
 // of the others), whose boxes land in the 128-byte-swizzled operand layout.
 bool make_tensor_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                      const uint64_t* strides, const uint32_t* box);
+
+// Map of a [rows, heads, channels] tensor (strides in elements) in boxes of 64 channels of one
+// head and `box_rows` rows; rows < 1 makes a map no copy may use.
+bool make_head_map(CUtensorMap* m, const void* ptr, int channels, int64_t heads, int64_t head,
+                   int64_t rows, int64_t token, uint32_t box_rows);
 
 // The device's SM count (148 on B200): the width of the persistent grids.
 int sm_count();
