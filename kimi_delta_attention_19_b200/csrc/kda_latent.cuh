@@ -33,7 +33,8 @@ struct AttnArgs {
   // backward
   const __nv_bfloat16 *o, *dout;
   const float* lse_in;
-  float *delta, *dpe_part;     // workspace: D_i [Tq_total, H]; [H, Tk_total, DP]
+  float2* stat;                // workspace: (lse log2 e, D) [H, Tq_total]
+  float* dpe_part;             // workspace: [H, Tk_total, DP]
   __nv_bfloat16 *dq, *dkn, *dkp, *dv;
 };
 

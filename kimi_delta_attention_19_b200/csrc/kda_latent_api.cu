@@ -74,14 +74,14 @@ bool bad_inputs(const void* q, const void* kn, const void* kp, const void* v,
 }
 
 struct BwdLayout {
-  size_t delta, dpe, total;
+  size_t stat, dpe, total;
 };
 
 BwdLayout bwd_layout(const kda_latent_shape& s) {
   BwdLayout l;
   const size_t tq = static_cast<size_t>(s.Tq) * s.B, tk = static_cast<size_t>(s.Tk) * s.B;
-  l.delta = 0;
-  l.dpe = align_up(tq * s.H * 4, 256);
+  l.stat = 0;
+  l.dpe = align_up(tq * s.H * 8, 256);
   l.total = align_up(l.dpe + tk * s.H * DP * 4, 256);
   if (l.total == 0) l.total = 256;
   return l;
@@ -170,7 +170,7 @@ kda_status kda_latent_attn_bwd(const void* q, const void* k_nope, const void* k_
   a.o = static_cast<const __nv_bfloat16*>(out);
   a.lse_in = lse;
   a.dout = static_cast<const __nv_bfloat16*>(d_out);
-  a.delta = reinterpret_cast<float*>(ws + l.delta);
+  a.stat = reinterpret_cast<float2*>(ws + l.stat);
   a.dpe_part = reinterpret_cast<float*>(ws + l.dpe);
   a.dq = static_cast<__nv_bfloat16*>(dq);
   a.dkn = static_cast<__nv_bfloat16*>(dk_nope);

@@ -1,130 +1,595 @@
-// kda_latent_bwd.cu -- expanded latent attention, backward: one warp a row.
-#include "kda_latent.cuh"
+// kda_latent_bwd.cu -- expanded latent attention, backward.
+//
+//   p_ij = exp(s_ij - lse_i)   dP = dO V^T   D_i = dO_i . out_i   dS = p (dP - D)
+//   dQ = scale dS K            dK = scale dS^T Q (k_pe: summed over heads)   dV = P^T dO
+//
+// Bound by the tensor cores. Scores and dP are formed twice, once a query tile (dQ) and once
+// a key tile (dK, dV): 2 x 1280 operations a pair instead of 2 x 960 with dQ accumulated across
+// key tiles, but every sum then stays in one CTA's tensor memory (192 columns of dQ, or
+// 128 + 192 of dV and dK), without atomics, so the same inputs give the same bits. Both kinds
+// of CTA are one launch, so that one kind fills the other's tail.
+//
+//   prepare   (lse log2 e, D) a (head, token), one array: the statistics of both kinds
+//   dQ CTA    128 queries, keys 128 at a time: S, dP [q, keys]; dS as bf16 in tensor memory,
+//             the A operand of dQ += dS K
+//   dK CTA    128 keys, queries 64 at a time (what tensor memory leaves): S^T, dP^T [keys, q];
+//             P^T and dS^T the A operands of dV += P^T dO and dK += dS^T Q
+//   k_pe      the heads' fp32 parts of dk_pe, summed in the heads' order
+//
+// In both, S of the next step is issued as soon as this step's is in registers, dP likewise,
+// so the products run beside the exponentials.
+#include "kda_latent_tc.cuh"
 
 namespace kda {
 namespace latent {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int BM = 128;                    // queries of a dQ CTA, keys of a dK CTA, key step of dQ
+constexpr int BQ = 64;                     // query step of a dK CTA
+constexpr uint32_t kAtom = BM * 128, kAtomQ = BQ * 128;
+constexpr int kQStages = 3;
+constexpr int kThreads = 384, kSoft = 256;
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  return x;
-}
+struct SmQ {  // dQ CTA
+  static constexpr uint32_t Q = 0, DO = 3 * kAtom, K = 5 * kAtom, V = 11 * kAtom, END = 13 * kAtom;
+};
+struct SmK {  // dK CTA
+  static constexpr uint32_t K = 0, V = 3 * kAtom, ST = 5 * kAtom, STAGE = 5 * kAtomQ,
+                            STAT = ST + kQStages * STAGE, END = STAT + 2 * BQ * 8;
+};
+constexpr uint32_t kBar = SmQ::END > SmK::END ? SmQ::END : SmK::END;
+constexpr uint32_t kTm = kBar + 256, kBail = kTm + 4, kBytes = kBail + 12;
+static_assert(kBytes <= 232448, "shared memory");
 
-// lane's channels of a row: 4 of k_nope / v (at 4 lane), 2 of k_pe (at 2 lane)
-__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xffff0000u);
-  x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xffff0000u);
-}
-__device__ __forceinline__ void ld2(const __nv_bfloat16* p, float (&x)[2]) {
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-  x[0] = __uint_as_float(w << 16); x[1] = __uint_as_float(w & 0xffff0000u);
-}
-__device__ __forceinline__ float dot4(const float (&a)[4], const float (&b)[4]) {
-  return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
-}
+struct Maps {
+  CUtensorMap q, qs, dout, douts, kn, kp, v;  // s: boxes of BQ rows
+};
 
-// First key query i does not see.
-__device__ __forceinline__ int key_end(const AttnArgs& a, const SeqRange& r, int i) {
-  return a.causal ? max(0, min(r.lk, i + 1 + r.lk - r.lq)) : r.lk;
-}
-
-__global__ void __launch_bounds__(kWarps * 32) dq_kernel(AttnArgs a) {
-  const int lane = threadIdx.x % 32, h = blockIdx.y;
-  SeqRange r;
-  if (!seq_range(a, blockIdx.z, r)) return;
-  const int i = blockIdx.x * kWarps + threadIdx.x / 32;
-  if (i >= r.lq) return;
-  const int64_t t = r.q0 + i, row = t * a.H + h;
-  float qn[4], qp[2], g[4], o[4], dn[4] = {0.f, 0.f, 0.f, 0.f}, dp[2] = {0.f, 0.f};
-  ld4(a.q + t * a.qt + h * a.qh + 4 * lane, qn);
-  ld2(a.q + t * a.qt + h * a.qh + DN + 2 * lane, qp);
-  ld4(a.dout + row * DV + 4 * lane, g);
-  ld4(a.o + row * DV + 4 * lane, o);
-  const float delta = warp_sum(dot4(g, o)), lse = a.lse_in[row];
-  if (lane == 0) a.delta[row] = delta;
-  const int end = key_end(a, r, i);
-  for (int j = 0; j < end; ++j) {
-    float kn[4], kp[2], v[4];
-    ld4(a.kn + (r.k0 + j) * a.kt + h * a.kh + 4 * lane, kn);
-    ld2(a.kp + (r.k0 + j) * a.pt + 2 * lane, kp);
-    ld4(a.v + (r.k0 + j) * a.vt + h * a.vh + 4 * lane, v);
-    const float s = a.scale * warp_sum(dot4(qn, kn) + qp[0] * kp[0] + qp[1] * kp[1]);
-    const float ds = a.scale * __expf(s - lse) * (warp_sum(dot4(g, v)) - delta);
+// (lse log2 e, D) of 32 tokens of a head a block; a row without keys gets +inf: p = 0.
+__global__ void __launch_bounds__(256) prepare_kernel(AttnArgs a, int64_t tq) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.y;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 32;
+  __shared__ float2 st[32];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) dn[x] += ds * kn[x];
+  for (int k = 0; k < 4; ++k) {
+    const int64_t t = t0 + warp * 4 + k;
+    if (t >= tq) break;
+    const int64_t row = t * a.H + h;
+    const uint2 x = *reinterpret_cast<const uint2*>(a.dout + row * DV + 4 * lane);
+    const uint2 y = *reinterpret_cast<const uint2*>(a.o + row * DV + 4 * lane);
+    auto lo = [](uint32_t b) { return __uint_as_float(b << 16); };
+    auto hi = [](uint32_t b) { return __uint_as_float(b & 0xffff0000u); };
+    float s = lo(x.x) * lo(y.x) + hi(x.x) * hi(y.x) + lo(x.y) * lo(y.y) + hi(x.y) * hi(y.y);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) dp[x] += ds * kp[x];
-  }
-#pragma unroll
-  for (int x = 0; x < 4; ++x) st_out(a.dq + row * DQK + 4 * lane + x, dn[x]);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) st_out(a.dq + row * DQK + DN + 2 * lane + x, dp[x]);
-}
-
-__global__ void __launch_bounds__(kWarps * 32) dkv_kernel(AttnArgs a, int64_t tk_total) {
-  const int lane = threadIdx.x % 32, h = blockIdx.y;
-  SeqRange r;
-  if (!seq_range(a, blockIdx.z, r)) return;
-  const int j = blockIdx.x * kWarps + threadIdx.x / 32;
-  if (j >= r.lk) return;
-  const int64_t t = r.k0 + j, row = t * a.H + h;
-  float kn[4], kp[2], v[4], dn[4] = {0.f, 0.f, 0.f, 0.f}, dp[2] = {0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-  ld4(a.kn + t * a.kt + h * a.kh + 4 * lane, kn);
-  ld2(a.kp + t * a.pt + 2 * lane, kp);
-  ld4(a.v + t * a.vt + h * a.vh + 4 * lane, v);
-  for (int i = a.causal ? max(0, j - (r.lk - r.lq)) : 0; i < r.lq; ++i) {
-    const int64_t qr = (r.q0 + i) * a.H + h;
-    float qn[4], qp[2], g[4];
-    ld4(a.q + (r.q0 + i) * a.qt + h * a.qh + 4 * lane, qn);
-    ld2(a.q + (r.q0 + i) * a.qt + h * a.qh + DN + 2 * lane, qp);
-    ld4(a.dout + qr * DV + 4 * lane, g);
-    const float s = a.scale * warp_sum(dot4(qn, kn) + qp[0] * kp[0] + qp[1] * kp[1]);
-    const float p = __expf(s - a.lse_in[qr]);
-    const float ds = a.scale * p * (warp_sum(dot4(g, v)) - a.delta[qr]);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      dn[x] += ds * qn[x];
-      dv[x] += p * g[x];
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (lane == 0) {
+      const float l = a.lse_in[row];
+      st[warp * 4 + k] = make_float2(l == -INFINITY ? INFINITY : l * kLog2e, s);
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) dp[x] += ds * qp[x];
   }
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    st_out(a.dkn + row * DN + 4 * lane + x, dn[x]);
-    st_out(a.dv + row * DV + 4 * lane + x, dv[x]);
+  __syncthreads();
+  if (threadIdx.x < 32 && t0 + threadIdx.x < tq)
+    a.stat[h * tq + t0 + threadIdx.x] = st[threadIdx.x];
+}
+
+__device__ __forceinline__ void zero_rows(unsigned char* tile, uint32_t atom, int atoms, int from,
+                                          int rows, int lane) {
+  const int per = atoms * 8;
+  for (int e = lane; e < (rows - from) * per; e += 32)
+    *reinterpret_cast<uint4*>(tile + sw128_chunk(from + e / per, e % per, atom)) =
+        make_uint4(0, 0, 0, 0);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_kernel(const __grid_constant__ Maps maps, const AttnArgs a, int64_t tq_all, int64_t tk_all,
+               int k_blocks, int q_blocks) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + kBar);
+  uint64_t *full = bar, *empty = bar + 3, *res_full = bar + 6, *s_full = bar + 7, *dp_full = bar + 8,
+           *s_read = bar + 9, *p_ready = bar + 10, *ds_ready = bar + 11, *p_free = bar + 12,
+           *ds_free = bar + 13, *o_full = bar + 14, *v_full = bar + 15, *v_empty = bar + 16,
+           *drain = bar + 17;
+  uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + kTm);
+  volatile int* bail = reinterpret_cast<volatile int*>(sm + kBail);
+  const uint32_t sb = smem_u32(sm);
+
+  // Key blocks first, those with the most queries ahead; then query blocks, likewise. Heads
+  // vary fastest.
+  const int blk = static_cast<int>(blockIdx.x / a.H), h = blockIdx.x % a.H;
+  const bool is_k = blk < k_blocks;
+  SeqRange r;
+  if (!seq_range(a, blockIdx.y, r)) return;
+  const int lag = r.lk - r.lq;  // causal: query i sees keys j <= i + lag
+  const int b0 = (is_k ? blk : k_blocks + q_blocks - 1 - blk) * BM;  // first key or query
+  if (b0 >= (is_k ? r.lk : r.lq)) return;
+  if (sb & 1023) {
+    if (tid == 0 && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
+    return;
   }
+  // steps [j0, j1) of queries (dK CTA) or keys (dQ CTA)
+  int j0 = 0, j1;
+  if (is_k) {
+    if (a.causal) j0 = max(0, b0 - lag) / BQ;
+    j1 = max(j0, (r.lq + BQ - 1) / BQ);
+  } else {
+    const int last = min(r.lq, b0 + BM);
+    j1 = (min(r.lk, a.causal ? max(0, last + lag) : r.lk) + BM - 1) / BM;
+  }
+  const int n = j1 - j0;
+
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(res_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(s_read, kSoft);
+    mbar_init(p_ready, kSoft);
+    mbar_init(ds_ready, kSoft);
+    mbar_init(p_free, 1);
+    mbar_init(ds_free, 1);
+    mbar_init(o_full, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *bail = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = *tmem;
+  const float sl = a.scale * kLog2e;
+  const float2 sl2 = make_float2(sl, sl);
+
+  if (is_k) {
+    // =================================================================== dK, dV
+    constexpr uint32_t S = 0, DP = 64, P = 128, DS = 160, DVC = 192, DK = 320;  // columns
+    if (warp == 0) {
+      if (n > 0 && elect_one()) {
+        const int kr = static_cast<int>(r.k0) + b0;
+        mbar_arrive_expect_tx(res_full, 5 * kAtom);
+        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmK::K + i * kAtom, &maps.kn, res_full, 64 * i, h, kr);
+        tma_load_2d(sm + SmK::K + 2 * kAtom, &maps.kp, res_full, 0, kr);
+        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmK::V + i * kAtom, &maps.v, res_full, 64 * i, h, kr);
+        int t = 0;
+        for (; t < n; ++t) {
+          const int s = t % kQStages, row = static_cast<int>(r.q0) + (j0 + t) * BQ;
+          if (t >= kQStages) wait_for(empty + s, (t / kQStages - 1) & 1, bail);
+          if (*bail) break;
+          unsigned char* st = sm + SmK::ST + s * SmK::STAGE;
+          mbar_arrive_expect_tx(full + s, SmK::STAGE);
+          for (int i = 0; i < 3; ++i) tma_load_3d(st + i * kAtomQ, &maps.qs, full + s, 64 * i, h, row);
+          for (int i = 0; i < 2; ++i) tma_load_3d(st + (3 + i) * kAtomQ, &maps.douts, full + s, 64 * i, h, row);
+        }
+        if (*bail) {  // let the copies in flight land before the CTA ends
+          mbar_wait(res_full, 0, 20000000LL);
+          for (int k = t > kQStages ? t - kQStages : 0; k < t; ++k)
+            mbar_wait(full + k % kQStages, k / kQStages & 1, 20000000LL);
+        }
+      }
+    } else if (warp == 1 && n > 0) {
+      constexpr uint32_t i64 = idesc_bf16(BM, BQ, 0, 0), iv = idesc_bf16(BM, 128, 0, 1),
+                         ik = idesc_bf16(BM, 192, 0, 1);
+      auto stage = [&](int t) { return sb + SmK::ST + t % kQStages * SmK::STAGE; };
+      auto scores = [&](int t) {  // S^T = K Q^T
+        wait_for(full + t % kQStages, t / kQStages & 1, bail);
+        const int valid = r.lq - (j0 + t) * BQ;
+        if (valid < BQ) {  // rows past the sequence may hold anything: 0 x NaN is NaN
+          zero_rows(sm + SmK::ST + t % kQStages * SmK::STAGE, kAtomQ, 5, valid, BQ, lane);
+          fence_async_smem();
+          __syncwarp();
+        }
+        const bool dead = bailed(bail);
+        tc_fence_after();
+        if (elect_one() && !dead) {
 #pragma unroll
-  for (int x = 0; x < 2; ++x) a.dpe_part[(h * tk_total + t) * DP + 2 * lane + x] = dp[x];
+          for (int i = 0; i < 3; ++i) {
+            const uint64_t ka = sdesc_sw128(sb + SmK::K + i * kAtom, 16, 1024);
+            const uint64_t qb = sdesc_sw128(stage(t) + i * kAtomQ, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(tb + S, ka + 2 * k, qb + 2 * k, i64, i > 0 || k > 0);
+          }
+          umma_commit(s_full);
+        }
+        __syncwarp();
+      };
+      auto dprobs = [&](int t) {  // dP^T = V dO^T
+        const bool dead = bailed(bail);
+        if (elect_one() && !dead) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t va = sdesc_sw128(sb + SmK::V + i * kAtom, 16, 1024);
+            const uint64_t gb = sdesc_sw128(stage(t) + (3 + i) * kAtomQ, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(tb + DP, va + 2 * k, gb + 2 * k, i64, i > 0 || k > 0);
+          }
+          umma_commit(dp_full);
+        }
+        __syncwarp();
+      };
+      wait_for(res_full, 0, bail);
+      scores(0);
+      dprobs(0);
+      for (int t = 0; t < n; ++t) {
+        wait_for(s_read, t & 1, bail);
+        if (t + 1 < n) scores(t + 1);
+        wait_for(p_ready, t & 1, bail);
+        bool dead = bailed(bail);
+        tc_fence_after();
+        if (elect_one() && !dead) {
+          const uint64_t gb = sdesc_sw128(stage(t) + 3 * kAtomQ, kAtomQ, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16_tmem_a(tb + DVC, tb + P + 8 * k, gb + 128 * k, iv, t > 0 || k > 0);
+          umma_commit(p_free);
+        }
+        __syncwarp();
+        wait_for(ds_ready, t & 1, bail);
+        tc_fence_after();
+        if (t + 1 < n) dprobs(t + 1);
+        dead = bailed(bail);
+        if (elect_one() && !dead) {
+          const uint64_t qb = sdesc_sw128(stage(t), kAtomQ, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16_tmem_a(tb + DK, tb + DS + 8 * k, qb + 128 * k, ik, t > 0 || k > 0);
+          umma_commit(ds_free);
+          umma_commit(empty + t % kQStages);
+          if (t + 1 == n) umma_commit(o_full);
+        }
+        __syncwarp();
+      }
+      if (bailed(bail)) {
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        mbar_wait(drain, 0, 20000000LL);
+      }
+    } else if (warp >= 4) {
+      const int g = (warp - 4) / 4, w = warp % 4;
+      const uint32_t lanes = tb + (static_cast<uint32_t>(w * 32) << 16);
+      const int j = b0 + w * 32 + lane;  // this thread's key
+      float2* stat = reinterpret_cast<float2*>(sm + SmK::STAT);
+      const float2* st_g = a.stat + h * tq_all + r.q0;
+      auto stat_of = [&](int t) {  // of query 32 g + lane of a step
+        const int i = (j0 + t) * BQ + 32 * g + lane;
+        return t < n && i < r.lq ? st_g[i] : make_float2(INFINITY, 0.f);
+      };
+      float2 next = w == 0 ? stat_of(0) : make_float2(0.f, 0.f);
+      for (int t = 0; t < n; ++t) {
+        float2* sd = stat + (t & 1) * BQ + 32 * g;
+        if (w == 0) {
+          sd[lane] = next;
+          next = stat_of(t + 1);
+        }
+        group_sync(1 + g, 128);
+        uint32_t v[32];
+        wait_for(s_full, t & 1, bail);
+        tc_fence_after();
+        tmem_ld32(lanes + S + 32 * g, v);
+        tmem_ld_wait(v);
+        tc_fence_before();
+        mbar_arrive(s_read);
+        const float4* sd4 = reinterpret_cast<const float4*>(sd);
+        float p[32];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float4 x = sd4[k / 2];
+          p[k] = ex2(__uint_as_float(v[k]) * sl - x.x);
+          p[k + 1] = ex2(__uint_as_float(v[k + 1]) * sl - x.z);
+        }
+        const int lim = j - lag - ((j0 + t) * BQ + 32 * g);  // queries below it do not see the key
+        if (a.causal && __any_sync(0xffffffffu, lim > 0)) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (k < lim) p[k] = 0.f;
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) pk[k] = pack2(p[2 * k], p[2 * k + 1]);
+        if (t > 0) wait_for(p_free, (t - 1) & 1, bail);
+        tmem_st16(lanes + P + 16 * g, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_ready);
+        wait_for(dp_full, t & 1, bail);
+        tc_fence_after();
+        tmem_ld32(lanes + DP + 32 * g, v);
+        tmem_ld_wait(v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float4 x = sd4[k];
+          pk[k] = pack2(p[2 * k] * (__uint_as_float(v[2 * k]) - x.y),
+                        p[2 * k + 1] * (__uint_as_float(v[2 * k + 1]) - x.w));
+        }
+        if (t > 0) wait_for(ds_free, (t - 1) & 1, bail);
+        tmem_st16(lanes + DS + 16 * g, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(ds_ready);
+      }
+      if (n > 0) wait_for(o_full, 0, bail);
+      tc_fence_after();
+      const bool mine = j < r.lk;
+      const int64_t tok = r.k0 + j, row = tok * a.H + h;
+      // dV: 64 columns a warpgroup; dK: 96 (the second one's last 64 are k_pe's)
+#pragma unroll 1
+      for (int q = 0; q < 10; ++q) {
+        uint32_t o[16];
+        const bool is_v = q < 4;
+        const int col = is_v ? 64 * g + 16 * q : 96 * g + 16 * (q - 4);
+        if (n > 0) {
+          tmem_ld16(lanes + (is_v ? DVC : DK) + col, o);
+          tmem_ld_wait(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = 0;
+        }
+        if (!mine) continue;
+        const float mul = is_v ? 1.f : a.scale;
+        if (!is_v && col >= DN) {
+          float4* dst = reinterpret_cast<float4*>(a.dpe_part + (h * tk_all + tok) * latent::DP + col - DN);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_float4(__uint_as_float(o[4 * k]) * mul, __uint_as_float(o[4 * k + 1]) * mul,
+                                 __uint_as_float(o[4 * k + 2]) * mul, __uint_as_float(o[4 * k + 3]) * mul);
+          continue;
+        }
+        uint4* dst = reinterpret_cast<uint4*>((is_v ? a.dv : a.dkn) + row * DN + col);
+        uint32_t x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          x[k] = pack2(__uint_as_float(o[2 * k]) * mul, __uint_as_float(o[2 * k + 1]) * mul);
+        dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+      }
+    }
+  } else {
+    // ======================================================================= dQ
+    constexpr uint32_t S = 0, DP = 128, DS = 256, DQ = 320;  // columns
+    if (warp == 0) {
+      if (n > 0 && elect_one()) {
+        const int qr = static_cast<int>(r.q0) + b0;
+        mbar_arrive_expect_tx(res_full, 5 * kAtom);
+        for (int i = 0; i < 3; ++i) tma_load_3d(sm + SmQ::Q + i * kAtom, &maps.q, res_full, 64 * i, h, qr);
+        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmQ::DO + i * kAtom, &maps.dout, res_full, 64 * i, h, qr);
+        int t = 0, tv = 0;
+        for (; t < n; ++t) {
+          const int s = t & 1, row = static_cast<int>(r.k0) + t * BM;
+          if (t >= 2) wait_for(empty + s, (t / 2 - 1) & 1, bail);
+          if (*bail) break;
+          unsigned char* st = sm + SmQ::K + s * 3 * kAtom;
+          mbar_arrive_expect_tx(full + s, 3 * kAtom);
+          for (int i = 0; i < 2; ++i) tma_load_3d(st + i * kAtom, &maps.kn, full + s, 64 * i, h, row);
+          tma_load_2d(st + 2 * kAtom, &maps.kp, full + s, 0, row);
+          if (t >= 1) wait_for(v_empty, (t - 1) & 1, bail);
+          if (*bail) { ++t; break; }
+          mbar_arrive_expect_tx(v_full, 2 * kAtom);
+          for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmQ::V + i * kAtom, &maps.v, v_full, 64 * i, h, row);
+          ++tv;
+        }
+        if (*bail) {  // let the copies in flight land before the CTA ends
+          mbar_wait(res_full, 0, 20000000LL);
+          for (int k = t > 2 ? t - 2 : 0; k < t; ++k) mbar_wait(full + (k & 1), k / 2 & 1, 20000000LL);
+          if (tv > 0) mbar_wait(v_full, (tv - 1) & 1, 20000000LL);
+        }
+      }
+    } else if (warp == 1 && n > 0) {
+      constexpr uint32_t i128 = idesc_bf16(BM, BM, 0, 0), iq = idesc_bf16(BM, 192, 0, 1);
+      auto scores = [&](int t) {  // S = Q K^T
+        wait_for(full + (t & 1), t / 2 & 1, bail);
+        const bool dead = bailed(bail);
+        tc_fence_after();
+        if (elect_one() && !dead) {
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const uint64_t qa = sdesc_sw128(sb + SmQ::Q + i * kAtom, 16, 1024);
+            const uint64_t kb = sdesc_sw128(sb + SmQ::K + ((t & 1) * 3 + i) * kAtom, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(tb + S, qa + 2 * k, kb + 2 * k, i128, i > 0 || k > 0);
+          }
+          umma_commit(s_full);
+        }
+        __syncwarp();
+      };
+      auto dprobs = [&](int t) {  // dP = dO V^T
+        wait_for(v_full, t & 1, bail);
+        const bool dead = bailed(bail);
+        tc_fence_after();
+        if (elect_one() && !dead) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t ga = sdesc_sw128(sb + SmQ::DO + i * kAtom, 16, 1024);
+            const uint64_t vb = sdesc_sw128(sb + SmQ::V + i * kAtom, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16(tb + DP, ga + 2 * k, vb + 2 * k, i128, i > 0 || k > 0);
+          }
+          umma_commit(dp_full);
+          umma_commit(v_empty);
+        }
+        __syncwarp();
+      };
+      wait_for(res_full, 0, bail);
+      scores(0);
+      dprobs(0);
+      for (int t = 0; t < n; ++t) {
+        wait_for(s_read, t & 1, bail);
+        if (t + 1 < n) scores(t + 1);
+        wait_for(ds_ready, t & 1, bail);
+        tc_fence_after();
+        if (t + 1 < n) dprobs(t + 1);
+        const int valid = r.lk - t * BM;
+        if (valid < BM) {  // rows past the sequence may hold anything: 0 x NaN is NaN
+          zero_rows(sm + SmQ::K + (t & 1) * 3 * kAtom, kAtom, 3, valid, BM, lane);
+          fence_async_smem();
+          __syncwarp();
+        }
+        const bool dead = bailed(bail);
+        if (elect_one() && !dead) {
+          const uint64_t kb = sdesc_sw128(sb + SmQ::K + (t & 1) * 3 * kAtom, kAtom, 1024);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_tmem_a(tb + DQ, tb + DS + 8 * k, kb + 128 * k, iq, t > 0 || k > 0);
+          umma_commit(ds_free);
+          umma_commit(empty + (t & 1));
+          if (t + 1 == n) umma_commit(o_full);
+        }
+        __syncwarp();
+      }
+      if (bailed(bail)) {
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        mbar_wait(drain, 0, 20000000LL);
+      }
+    } else if (warp >= 4) {
+      const int g = (warp - 4) / 4, w = warp % 4;  // g: half of the keys of a step
+      const uint32_t lanes = tb + (static_cast<uint32_t>(w * 32) << 16);
+      const int i = b0 + w * 32 + lane;            // this thread's query
+      const bool mine = i < r.lq;
+      const float2 st = mine ? a.stat[h * tq_all + r.q0 + i] : make_float2(INFINITY, 0.f);
+      const int kend = a.causal ? min(r.lk, max(0, i + 1 + lag)) : r.lk;
+      const float2 nl2 = make_float2(-st.x, -st.x), nd2 = make_float2(-st.y, -st.y);
+      for (int t = 0; t < n; ++t) {
+        wait_for(s_full, t & 1, bail);
+        tc_fence_after();
+        uint32_t v[2][32];
+        tmem_ld32(lanes + S + 64 * g, v[0]);
+        tmem_ld32(lanes + S + 64 * g + 32, v[1]);
+        tmem_ld_wait(v[0]);
+        tmem_ld_wait(v[1]);
+        tc_fence_before();
+        mbar_arrive(s_read);
+        float2 p[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float2 x = fma2(make_float2(__uint_as_float(v[k / 16][k % 16 * 2]),
+                                            __uint_as_float(v[k / 16][k % 16 * 2 + 1])), sl2, nl2);
+          p[k] = make_float2(ex2(x.x), ex2(x.y));
+        }
+        const int lim = kend - t * BM - 64 * g;  // keys of this half the query sees
+        const bool cut = __any_sync(0xffffffffu, lim < 64);
+        wait_for(dp_full, t & 1, bail);
+        tc_fence_after();
+        tmem_ld32(lanes + DP + 64 * g, v[0]);
+        tmem_ld32(lanes + DP + 64 * g + 32, v[1]);
+        tmem_ld_wait(v[0]);
+        tmem_ld_wait(v[1]);
+        uint32_t ds[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float2 x = mul2f(p[k], add2(make_float2(__uint_as_float(v[k / 16][k % 16 * 2]),
+                                                        __uint_as_float(v[k / 16][k % 16 * 2 + 1])), nd2));
+          ds[k] = pack2(x.x, x.y);
+        }
+        if (cut) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (2 * k >= lim) ds[k] &= 0xffff0000u;
+            if (2 * k + 1 >= lim) ds[k] &= 0x0000ffffu;
+          }
+        }
+        if (t > 0) wait_for(ds_free, (t - 1) & 1, bail);
+        tmem_st32(lanes + DS + 32 * g, ds);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(ds_ready);
+      }
+      if (n > 0) wait_for(o_full, 0, bail);
+      tc_fence_after();
+      const int64_t row = (r.q0 + i) * a.H + h;
+#pragma unroll 1
+      for (int q = 0; q < 6; ++q) {
+        uint32_t o[16];
+        if (n > 0) {
+          tmem_ld16(lanes + DQ + 96 * g + 16 * q, o);
+          tmem_ld_wait(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = 0;
+        }
+        if (!mine) continue;
+        uint4* dst = reinterpret_cast<uint4*>(a.dq + row * DQK + 96 * g + 16 * q);
+        uint32_t x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          x[k] = pack2(__uint_as_float(o[2 * k]) * a.scale, __uint_as_float(o[2 * k + 1]) * a.scale);
+        dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *bail && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
 }
 
 // dk_pe = the heads' parts, summed in the heads' order
-__global__ void dpe_kernel(AttnArgs a, int64_t tk_total) {
+__global__ void __launch_bounds__(256) dpe_kernel(AttnArgs a, int64_t tk_all) {
   SeqRange r;
-  if (!seq_range(a, blockIdx.z, r)) return;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (e >= static_cast<int64_t>(r.lk) * DP) return;
-  const int64_t at = r.k0 * DP + e;
-  float s = 0.f;
-  for (int h = 0; h < a.H; ++h) s += a.dpe_part[h * tk_total * DP + at];
-  st_out(a.dkp + at, s);
+  if (!seq_range(a, blockIdx.y, r)) return;
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // four channels
+  if (e >= static_cast<int64_t>(r.lk) * (DP / 4)) return;
+  const int64_t at = r.k0 * (DP / 4) + e;
+  const float4* part = reinterpret_cast<const float4*>(a.dpe_part);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int h = 0; h < a.H; ++h) {
+    const float4 x = part[h * tk_all * (DP / 4) + at];
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  }
+  reinterpret_cast<uint2*>(a.dkp)[at] = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
 }
 
-unsigned blocks(int64_t n, int per) { return static_cast<unsigned>((n + per - 1) / per); }
+int64_t blocks(int64_t n, int per) { return (n + per - 1) / per; }
 
 }  // namespace
 
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t st) {
-  const int64_t tk_total = a.cu_k != nullptr ? a.Tk : a.Tk * a.n_seqs;
-  if (a.max_q > 0) dq_kernel<<<dim3(blocks(a.max_q, kWarps), a.H, a.n_seqs), kWarps * 32, 0, st>>>(a);
-  if (a.max_k > 0) {
-    dkv_kernel<<<dim3(blocks(a.max_k, kWarps), a.H, a.n_seqs), kWarps * 32, 0, st>>>(a, tk_total);
-    dpe_kernel<<<dim3(blocks(a.max_k * DP, 256), 1, a.n_seqs), 256, 0, st>>>(a, tk_total);
+  const int64_t tq = a.cu_q != nullptr ? a.Tq : a.Tq * a.n_seqs;
+  const int64_t tk = a.cu_k != nullptr ? a.Tk : a.Tk * a.n_seqs;
+  Maps m;
+  memset(&m, 0, sizeof m);
+  const int64_t ot = static_cast<int64_t>(a.H) * DV;
+  if (!make_head_map(&m.q, a.q, DQK, a.H, a.qh, tq, a.qt, BM) ||
+      !make_head_map(&m.qs, a.q, DQK, a.H, a.qh, tq, a.qt, BQ) ||
+      !make_head_map(&m.dout, a.dout, DV, a.H, DV, tq, ot, BM) ||
+      !make_head_map(&m.douts, a.dout, DV, a.H, DV, tq, ot, BQ) ||
+      !make_head_map(&m.kn, a.kn, DN, a.H, a.kh, tk, a.kt, BM) ||
+      !make_head_map(&m.v, a.v, DV, a.H, a.vh, tk, a.vt, BM))
+    return cudaErrorInvalidValue;
+  if (tk > 0) {
+    const uint64_t dims[2] = {DP, static_cast<uint64_t>(tk)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(a.pt) * 2};
+    const uint32_t box[2] = {64, BM};
+    if (!make_tensor_map(&m.kp, a.kp, 2, dims, strides, box)) return cudaErrorInvalidValue;
   }
+  cudaError_t e = cudaFuncSetAttribute(bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kBytes);
+  if (e != cudaSuccess) return e;
+  if (tq > 0)
+    prepare_kernel<<<dim3(static_cast<unsigned>(blocks(tq, 32)), a.H), 256, 0, st>>>(a, tq);
+  const int64_t kb = blocks(a.max_k, BM), qb = blocks(a.max_q, BM);
+  if ((kb + qb) * a.H > 0x7fffffff) return cudaErrorInvalidValue;
+  bwd_kernel<<<dim3(static_cast<unsigned>((kb + qb) * a.H), a.n_seqs), kThreads, kBytes, st>>>(
+      m, a, tq, tk, static_cast<int>(kb), static_cast<int>(qb));
+  if (a.max_k > 0)
+    dpe_kernel<<<dim3(static_cast<unsigned>(blocks(a.max_k * (DP / 4), 256)), a.n_seqs), 256, 0,
+                 st>>>(a, tk);
   return cudaGetLastError();
 }
 
