@@ -15,7 +15,6 @@ device and on `stream` (default: that device's current stream).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -74,43 +73,51 @@ EXPORTED = ("kda_latent_attn_fwd", "kda_latent_attn_bwd_workspace_size", "kda_la
             "kda_latent_decode_workspace_size", "kda_latent_decode")
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
-def _bf16(t: torch.Tensor, name: str) -> None:
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"unsupported dtype {t.dtype} of {name}: latent attention takes bfloat16")
-
-
-def _typed(t: torch.Tensor | None, dtype: torch.dtype, shape, name: str, like: torch.Tensor):
-    """Checks an optional contiguous tensor argument on `like`'s device."""
+# The checks of a call are plain conditions (messages are formed only when one fails), pointers
+# and streams go to the library as integers and structs are filled by position: a call that
+# launches one small kernel costs the host more than the GPU otherwise.
+def _typed(t: torch.Tensor | None, dtype: torch.dtype, shape, name: str, device) -> int | None:
+    """Checks an optional contiguous tensor argument on `device`; its address."""
     if t is None:
-        return
+        return None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if shape is not None:
-        _need(tuple(t.shape) == tuple(shape),
-              f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
-    _need(t.device == like.device, f"{name} is on {t.device}, not on {like.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
 
 
-def _addr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _bf16(t: torch.Tensor, name: str, device) -> None:
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}: latent attention takes bfloat16")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-@contextlib.contextmanager
-def _on(t: torch.Tensor, stream):
-    """The tensors' device and the stream of the call, current while scratch is allocated."""
-    _need(t.is_cuda, f"latent attention needs CUDA tensors (got {t.device})")
-    with torch.cuda.device(t.device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
+def _launch(device: torch.device, stream, call):
+    """`call(raw stream)` with the tensors' device and the call's stream current (so that
+    what it allocates belongs to them). Without a GPU tensor it refuses."""
+    if device.type != "cuda":
+        raise ValueError(f"latent attention needs CUDA tensors (got {device})")
+    if stream is not None:
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return call(_raw_stream(device.index))
+    return call(_raw_stream(device.index))
+
+
+def _addr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _check(rc: int, what: str) -> None:
@@ -119,54 +126,56 @@ def _check(rc: int, what: str) -> None:
 
 
 # ------------------------------------------------------------------------ expanded form
+def _strides(t: torch.Tensor, name: str, batched: bool):
+    """(token, head) strides of [.., T, H, d], or (token, 0) of k_pe [.., T, d], in elements."""
+    head = name != "k_pe"
+    st, shape = t.stride(), t.shape
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    token = st[-3] if head else st[-2]
+    if batched and shape[0] != 1 and st[0] != token * shape[1] and t.numel() != 0:
+        raise ValueError(f"{name}'s sequences must follow each other (strides {st})")
+    # of a dimension of one the stride says nothing
+    hs = (st[-2] if shape[-2] > 1 else shape[-1]) if head else 0
+    if (shape[-3] if head else shape[-2]) <= 1 and not (batched and shape[0] > 1):
+        token = max(hs * (shape[-2] if head else 0), shape[-1])
+    return token, hs
+
+
 def _attn_shape(q, k_nope, k_pe, v, cu_q, cu_k, max_q, max_k, causal, scale):
-    for t, name in ((q, "q"), (k_nope, "k_nope"), (k_pe, "k_pe"), (v, "v")):
-        _bf16(t, name)
-        _need(t.device == q.device, f"{name} is on {t.device}, not on {q.device}")
-    batched = q.dim() == 4
-    _need(q.dim() in (3, 4) and k_nope.dim() == q.dim() and v.dim() == q.dim()
-          and k_pe.dim() == q.dim() - 1, "q, k_nope, v must be [T, H, d] or [B, T, H, d] and "
-          "k_pe [T, d] or [B, T, d]")
-    H = q.shape[-2]
-    lead_k = tuple(k_nope.shape[:-2])
-    _need(k_nope.shape[-2] == H and v.shape[-2] == H and tuple(v.shape[:-2]) == lead_k
-          and tuple(k_pe.shape[:-1]) == lead_k
-          and (not batched or q.shape[0] == k_nope.shape[0]),
-          f"shapes do not agree: q {tuple(q.shape)}, k_nope {tuple(k_nope.shape)}, "
-          f"k_pe {tuple(k_pe.shape)}, v {tuple(v.shape)}")
-    _need(q.shape[-1] == k_nope.shape[-1] + k_pe.shape[-1],
-          "q's channels must be k_nope's and k_pe's together")
-    _need((cu_q is None) == (cu_k is None) and not (batched and cu_q is not None),
-          "cu_seqlens takes packed [T, H, d] inputs, for queries and keys alike")
+    dev, qs, ks, vs, ps = q.device, q.shape, k_nope.shape, v.shape, k_pe.shape
+    _bf16(q, "q", dev)
+    _bf16(k_nope, "k_nope", dev)
+    _bf16(k_pe, "k_pe", dev)
+    _bf16(v, "v", dev)
+    dim = len(qs)
+    batched = dim == 4
+    if dim not in (3, 4) or len(ks) != dim or len(vs) != dim or len(ps) != dim - 1:
+        raise ValueError("q, k_nope, v must be [T, H, d] or [B, T, H, d] and k_pe [T, d] or "
+                         "[B, T, d]")
+    H = qs[-2]
+    if ks[-2] != H or vs[:-1] != ks[:-1] or ps[:-1] != ks[:-2] or (batched and qs[0] != ks[0]):
+        raise ValueError(f"shapes do not agree: q {tuple(qs)}, k_nope {tuple(ks)}, "
+                         f"k_pe {tuple(ps)}, v {tuple(vs)}")
+    if qs[-1] != ks[-1] + ps[-1]:
+        raise ValueError("q's channels must be k_nope's and k_pe's together")
+    if (cu_q is None) != (cu_k is None) or (batched and cu_q is not None):
+        raise ValueError("cu_seqlens takes packed [T, H, d] inputs, for queries and keys alike")
+    n_seqs = 0
     if cu_q is not None:
-        _typed(cu_q, torch.int32, None, "cu_seqlens", q)
-        _typed(cu_k, torch.int32, cu_q.shape, "cu_seqlens_k", q)
-        _need(cu_q.dim() == 1 and cu_q.numel() >= 2, "cu_seqlens must hold n_seqs + 1 offsets")
-
-    def strides(t, name, head=True):
-        s = t.stride()
-        _need(s[-1] == 1 or t.shape[-1] == 1, f"{name}'s channels must be contiguous")
-        token = s[-3] if head else s[-2]
-        if batched:   # sequence after sequence
-            _need(t.shape[0] == 1 or s[0] == token * t.shape[1] or t.numel() == 0,
-                  f"{name}'s sequences must follow each other (strides {s})")
-        # of a dimension of one the stride says nothing
-        hs = (s[-2] if t.shape[-2] > 1 else t.shape[-1]) if head else 0
-        n = t.shape[-3] if head else t.shape[-2]
-        if n <= 1 and not (batched and t.shape[0] > 1):
-            token = max(hs * (t.shape[-2] if head else 0), t.shape[-1])
-        return token, hs
-
-    qt, qh = strides(q, "q")
-    kt, kh = strides(k_nope, "k_nope")
-    vt, vh = strides(v, "v")
-    pt, _ = strides(k_pe, "k_pe", head=False)
-    return LatentShape(B=q.shape[0] if batched else 1, H=H, Tq=q.shape[-3], Tk=k_nope.shape[-3],
-                       n_seqs=0 if cu_q is None else cu_q.numel() - 1, max_q=int(max_q),
-                       max_k=int(max_k), d_nope=k_nope.shape[-1], d_pe=k_pe.shape[-1],
-                       d_v=v.shape[-1], q_token=qt, q_head=qh, k_token=kt, k_head=kh,
-                       pe_token=pt, v_token=vt, v_head=vh, causal=int(bool(causal)),
-                       dtype=KDA_BF16, scale=0.0 if scale is None else float(scale))
+        if cu_q.dim() != 1 or cu_q.numel() < 2:
+            raise ValueError("cu_seqlens must hold n_seqs + 1 offsets")
+        _typed(cu_q, torch.int32, None, "cu_seqlens", dev)
+        if cu_k is not cu_q:
+            _typed(cu_k, torch.int32, cu_q.shape, "cu_seqlens_k", dev)
+        n_seqs = cu_q.numel() - 1
+    qt, qh = _strides(q, "q", batched)
+    kt, kh = _strides(k_nope, "k_nope", batched)
+    vt, vh = _strides(v, "v", batched)
+    pt, _ = _strides(k_pe, "k_pe", batched)
+    return LatentShape(qs[0] if batched else 1, H, qs[-3], ks[-3], n_seqs, int(max_q),
+                       int(max_k), ks[-1], ps[-1], vs[-1], qt, qh, kt, kh, pt, vt, vh,
+                       int(bool(causal)), KDA_BF16, 0.0 if scale is None else float(scale))
 
 
 def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
@@ -190,19 +199,22 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
     s = _attn_shape(q, k_nope, k_pe, v, cu_seqlens, cu_seqlens_k, max_seqlen, max_seqlen_k,
                     causal, scale)
-    lead = tuple(q.shape[:-1])
-    _typed(out, torch.bfloat16, lead + (v.shape[-1],), "out", q)
-    _typed(lse, torch.float32, lead, "lse", q)
-    _typed(status, torch.int32, None, "status", q)
-    with _on(q, stream) as st:
+    dev, lead = q.device, q.shape[:-1]
+    _typed(out, torch.bfloat16, lead + v.shape[-1:], "out", dev)
+    _typed(lse, torch.float32, lead, "lse", dev)
+    status_p = _typed(status, torch.int32, None, "status", dev)
+
+    def call(st):
+        nonlocal out, lse
         if out is None:
-            out = torch.empty(lead + (v.shape[-1],), dtype=q.dtype, device=q.device)
+            out = torch.empty(lead + v.shape[-1:], dtype=q.dtype, device=dev)
         if lse is None:
-            lse = torch.empty(lead, dtype=torch.float32, device=q.device)
-        _check(lib.kda_latent_attn_fwd(_addr(q), _addr(k_nope), _addr(k_pe), _addr(v),
-                                       _addr(cu_seqlens), _addr(cu_seqlens_k), _addr(out),
-                                       _addr(lse), ctypes.byref(s), _addr(status), st),
-               "kda_latent_attn_fwd")
+            lse = torch.empty(lead, dtype=torch.float32, device=dev)
+        return lib.kda_latent_attn_fwd(
+            q.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), v.data_ptr(), _addr(cu_seqlens),
+            _addr(cu_seqlens_k), out.data_ptr(), lse.data_ptr(), ctypes.byref(s), status_p, st)
+
+    _check(_launch(dev, stream, call), "kda_latent_attn_fwd")
     return out, lse
 
 
@@ -222,31 +234,34 @@ def latent_attn_bwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
     s = _attn_shape(q, k_nope, k_pe, v, cu_seqlens, cu_seqlens_k, max_seqlen, max_seqlen_k,
                     causal, scale)
-    lead = tuple(q.shape[:-1])
-    _typed(out, torch.bfloat16, lead + (v.shape[-1],), "out", q)
-    _typed(lse, torch.float32, lead, "lse", q)
-    _typed(d_out, torch.bfloat16, lead + (v.shape[-1],), "d_out", q)
-    _typed(status, torch.int32, None, "status", q)
-    _typed(workspace, torch.uint8, None, "workspace", q)
-    names = (("dq", q), ("dk_nope", k_nope), ("dk_pe", k_pe), ("dv", v))
+    dev, lead = q.device, q.shape[:-1]
+    out_p = _typed(out, torch.bfloat16, lead + v.shape[-1:], "out", dev)
+    lse_p = _typed(lse, torch.float32, lead, "lse", dev)
+    d_out_p = _typed(d_out, torch.bfloat16, lead + v.shape[-1:], "d_out", dev)
+    status_p = _typed(status, torch.int32, None, "status", dev)
+    _typed(workspace, torch.uint8, None, "workspace", dev)
+    like = (q, k_nope, k_pe, v)
     if grads is not None:
-        _need(len(grads) == 4, "grads must be (dq, dk_nope, dk_pe, dv)")
-        for g, (name, like) in zip(grads, names):
-            _typed(g, torch.bfloat16, like.shape, name, q)
-    with _on(q, stream) as st:
+        if len(grads) != 4:
+            raise ValueError("grads must be (dq, dk_nope, dk_pe, dv)")
+        for g, t, name in zip(grads, like, ("dq", "dk_nope", "dk_pe", "dv")):
+            _typed(g, torch.bfloat16, t.shape, name, dev)
+
+    def call(st):
+        nonlocal grads, workspace
         if grads is None:
-            grads = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                          for _, t in names)
+            grads = tuple(torch.empty(t.shape, dtype=t.dtype, device=dev) for t in like)
         if workspace is None:
-            nbytes = int(lib.kda_latent_attn_bwd_workspace_size(ctypes.byref(s)))
+            nbytes = lib.kda_latent_attn_bwd_workspace_size(ctypes.byref(s))
             if nbytes == 0:
                 raise KdaError(KDA_ERR_INVALID_ARG, "kda_latent_attn_bwd_workspace_size")
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        _check(lib.kda_latent_attn_bwd(_addr(q), _addr(k_nope), _addr(k_pe), _addr(v),
-                                       _addr(out), _addr(lse), _addr(d_out), _addr(cu_seqlens),
-                                       _addr(cu_seqlens_k), *(_addr(g) for g in grads),
-                                       ctypes.byref(s), _addr(workspace), workspace.numel(),
-                                       _addr(status), st), "kda_latent_attn_bwd")
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return lib.kda_latent_attn_bwd(
+            q.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), v.data_ptr(), out_p, lse_p,
+            d_out_p, _addr(cu_seqlens), _addr(cu_seqlens_k), *(g.data_ptr() for g in grads),
+            ctypes.byref(s), workspace.data_ptr(), workspace.numel(), status_p, st)
+
+    _check(_launch(dev, stream, call), "kda_latent_attn_bwd")
     return tuple(grads)
 
 
@@ -292,23 +307,28 @@ def latent_cache(n_pages: int, page_size: int = 64, *, quantized: bool = False,
                  device="cuda") -> torch.Tensor:
     """A paged cache, zeros: bf16 [n_pages, page_size, 576], or with `quantized` 8-bit rows,
     uint8 [n_pages, page_size, 656]. page_size is 16, 32, 64 or 128."""
-    _need(page_size in (16, 32, 64, 128), f"page_size must be 16, 32, 64 or 128 ({page_size})")
+    if page_size not in (16, 32, 64, 128):
+        raise ValueError(f"page_size must be 16, 32, 64 or 128 ({page_size})")
     if quantized:
         return torch.zeros(n_pages, page_size, E4M3_ROW_BYTES, dtype=torch.uint8, device=device)
     return torch.zeros(n_pages, page_size, D_C + D_PE, dtype=torch.bfloat16, device=device)
 
 
+_FORMATS = {torch.bfloat16: (CACHE_BF16, D_C + D_PE), torch.uint8: (CACHE_E4M3, E4M3_ROW_BYTES)}
+
+
 def _cache_shape(cache: torch.Tensor) -> CacheShape:
-    _need(cache.dim() == 3, f"cache must be [n_pages, page_size, row] (got {tuple(cache.shape)})")
-    fmt, row = {torch.bfloat16: (CACHE_BF16, D_C + D_PE),
-                torch.uint8: (CACHE_E4M3, E4M3_ROW_BYTES)}.get(cache.dtype, (None, 0))
+    shape = cache.shape
+    if len(shape) != 3:
+        raise ValueError(f"cache must be [n_pages, page_size, row] (got {tuple(shape)})")
+    fmt = _FORMATS.get(cache.dtype)
     if fmt is None:
         raise TypeError(f"unsupported cache dtype {cache.dtype}: bfloat16 or uint8 rows")
-    _need(cache.shape[2] == row, f"a {cache.dtype} cache row has {row} values "
-          f"(got {cache.shape[2]})")
-    _need(cache.is_contiguous(), "cache must be contiguous")
-    return CacheShape(n_pages=cache.shape[0], page_size=cache.shape[1], d_c=D_C, d_pe=D_PE,
-                      format=fmt)
+    if shape[2] != fmt[1]:
+        raise ValueError(f"a {cache.dtype} cache row has {fmt[1]} values (got {shape[2]})")
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    return CacheShape(shape[0], shape[1], D_C, D_PE, fmt[0])
 
 
 def latent_cache_write(latent: torch.Tensor, k_pe: torch.Tensor, cache: torch.Tensor,
@@ -318,21 +338,20 @@ def latent_cache_write(latent: torch.Tensor, k_pe: torch.Tensor, cache: torch.Te
     strided) to rows slots [T] (int64: page * page_size + offset). Negative slots are
     skipped (padding); one past the cache is skipped and reported as 3 in `status` (int32
     device tensor). Slots must be distinct."""
-    cs = _cache_shape(cache)
+    cs, dev, T = _cache_shape(cache), cache.device, latent.shape[0]
     for t, name, d in ((latent, "latent", D_C), (k_pe, "k_pe", D_PE)):
-        _bf16(t, name)
-        _need(t.dim() == 2 and t.shape[1] == d and t.stride(1) == 1,
-              f"{name} must be [T, {d}] with contiguous channels")
-        _need(t.device == cache.device, f"{name} is on {t.device}, not on {cache.device}")
-    T = latent.shape[0]
-    _need(k_pe.shape[0] == T, "latent and k_pe must have the same tokens")
-    _typed(slots, torch.int64, (T,), "slots", cache)
-    _typed(status, torch.int32, None, "status", cache)
-    strides = [t.stride(0) if T > 1 else t.shape[1] for t in (latent, k_pe)]
-    with _on(cache, stream) as st:
-        _check(lib.kda_latent_cache_write(_addr(latent), strides[0], _addr(k_pe), strides[1],
-                                          _addr(slots), T, _addr(cache), ctypes.byref(cs),
-                                          _addr(status), st), "kda_latent_cache_write")
+        _bf16(t, name, dev)
+        if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1:
+            raise ValueError(f"{name} must be [T, {d}] with contiguous channels")
+    if k_pe.shape[0] != T:
+        raise ValueError("latent and k_pe must have the same tokens")
+    slots_p = _typed(slots, torch.int64, latent.shape[:1], "slots", dev)
+    status_p = _typed(status, torch.int32, None, "status", dev)
+    args = (latent.data_ptr(), latent.stride(0) if T > 1 else D_C, k_pe.data_ptr(),
+            k_pe.stride(0) if T > 1 else D_PE, slots_p, T, cache.data_ptr(), ctypes.byref(cs),
+            status_p)
+    _check(_launch(dev, stream, lambda st: lib.kda_latent_cache_write(*args, st)),
+           "kda_latent_cache_write")
 
 
 def latent_cache_read(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -344,27 +363,31 @@ def latent_cache_read(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens
     then k_pe), for instance to expand a cached prefix in front of new queries. block_table
     is int32 [n, pages]. A token past its table or with a page out of range is NaN and
     reported as 3 in `status`; rows behind the last sequence are not written."""
-    cs = _cache_shape(cache)
-    _typed(cu_seqlens, torch.int32, None, "cu_seqlens", cache)
-    _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2,
-          "cu_seqlens must hold n_seqs + 1 offsets")
+    cs, dev = _cache_shape(cache), cache.device
+    cu_p = _typed(cu_seqlens, torch.int32, None, "cu_seqlens", dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold n_seqs + 1 offsets")
     n = cu_seqlens.numel() - 1
-    _typed(block_table, torch.int32, None, "block_table", cache)
-    _need(block_table.dim() == 2 and block_table.shape[0] == n,
-          f"block_table must be [{n}, pages] (got {tuple(block_table.shape)})")
-    _typed(starts, torch.int32, (n,), "starts", cache)
-    _typed(status, torch.int32, None, "status", cache)
-    _need(total is not None or out is not None, "total (rows of the result) or out is needed")
+    table_p = _typed(block_table, torch.int32, None, "block_table", dev)
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError(f"block_table must be [{n}, pages] (got {tuple(block_table.shape)})")
+    starts_p = _typed(starts, torch.int32, (n,), "starts", dev)
+    status_p = _typed(status, torch.int32, None, "status", dev)
     if out is not None:
         _typed(out, torch.bfloat16, (out.shape[0] if total is None else total, D_C + D_PE),
-               "out", cache)
-    with _on(cache, stream) as st:
+               "out", dev)
+    elif total is None:
+        raise ValueError("total (rows of the result) or out is needed")
+
+    def call(st):
+        nonlocal out
         if out is None:
-            out = torch.empty(total, D_C + D_PE, dtype=torch.bfloat16, device=cache.device)
-        _check(lib.kda_latent_cache_read(_addr(cache), _addr(block_table), block_table.shape[1],
-                                         _addr(cu_seqlens), _addr(starts), n, out.shape[0],
-                                         _addr(out), ctypes.byref(cs), _addr(status), st),
-               "kda_latent_cache_read")
+            out = torch.empty(total, D_C + D_PE, dtype=torch.bfloat16, device=dev)
+        return lib.kda_latent_cache_read(cache.data_ptr(), table_p, block_table.shape[1], cu_p,
+                                         starts_p, n, out.shape[0], out.data_ptr(),
+                                         ctypes.byref(cs), status_p, st)
+
+    _check(_launch(dev, stream, call), "kda_latent_cache_read")
     return out
 
 
@@ -388,34 +411,37 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     out = 0, lse = -inf. seq_lens past the table or a page out of range: NaN rows and 3 in
     `status`. `workspace` may be kept (latent_decode_workspace); it serves one call at a time.
     """
-    cs = _cache_shape(cache)
-    _bf16(q, "q")
-    _need(q.dim() in (3, 4) and q.shape[-1] == D_C + D_PE,
-          f"q must be [N, H, {D_C + D_PE}] or [N, L, H, {D_C + D_PE}] (got {tuple(q.shape)})")
-    N, L, H = q.shape[0], q.shape[1] if q.dim() == 4 else 1, q.shape[-2]
-    lead = tuple(q.shape[:-1])
-    _typed(q, torch.bfloat16, None, "q", cache)
-    _typed(block_table, torch.int32, None, "block_table", cache)
-    _need(block_table.dim() == 2 and block_table.shape[0] == N,
-          f"block_table must be [{N}, pages] (got {tuple(block_table.shape)})")
-    _typed(seq_lens, torch.int32, (N,), "seq_lens", cache)
-    _typed(draft_mask, torch.int64, (N, L), "draft_mask", cache)
-    _typed(out, torch.bfloat16, lead + (D_C,), "out", cache)
-    _typed(lse, torch.float32, lead, "lse", cache)
-    _typed(workspace, torch.uint8, None, "workspace", cache)
-    _typed(status, torch.int32, None, "status", cache)
-    s = DecodeShape(N=N, L=L, H=H, table_pages=block_table.shape[1], dtype=KDA_BF16,
-                    scale=0.0 if scale is None else float(scale))
-    with _on(cache, stream) as st:
+    cs, dev, qs = _cache_shape(cache), cache.device, q.shape
+    _bf16(q, "q", dev)
+    dim = len(qs)
+    if dim not in (3, 4) or qs[-1] != D_C + D_PE:
+        raise ValueError(f"q must be [N, H, {D_C + D_PE}] or [N, L, H, {D_C + D_PE}] "
+                         f"(got {tuple(qs)})")
+    N, L, H = qs[0], qs[1] if dim == 4 else 1, qs[-2]
+    lead = qs[:-1]
+    q_p = _typed(q, torch.bfloat16, None, "q", dev)
+    table_p = _typed(block_table, torch.int32, None, "block_table", dev)
+    if block_table.dim() != 2 or block_table.shape[0] != N:
+        raise ValueError(f"block_table must be [{N}, pages] (got {tuple(block_table.shape)})")
+    lens_p = _typed(seq_lens, torch.int32, (N,), "seq_lens", dev)
+    mask_p = _typed(draft_mask, torch.int64, (N, L), "draft_mask", dev)
+    _typed(out, torch.bfloat16, lead + (D_C,), "out", dev)
+    lse_p = _typed(lse, torch.float32, lead, "lse", dev)
+    _typed(workspace, torch.uint8, None, "workspace", dev)
+    status_p = _typed(status, torch.int32, None, "status", dev)
+    s = DecodeShape(N, L, H, block_table.shape[1], KDA_BF16, 0.0 if scale is None else float(scale))
+
+    def call(st):
+        nonlocal out, workspace
         if out is None:
-            out = torch.empty(lead + (D_C,), dtype=torch.bfloat16, device=q.device)
+            out = torch.empty(lead + (D_C,), dtype=torch.bfloat16, device=dev)
         if workspace is None:
-            workspace = _decode_workspace(s, cs, q.device)
-        _check(lib.kda_latent_decode(_addr(q), _addr(cache), _addr(block_table),
-                                     _addr(seq_lens), _addr(draft_mask), _addr(out), _addr(lse),
-                                     ctypes.byref(s), ctypes.byref(cs), _addr(workspace),
-                                     workspace.numel(), _addr(status), st),
-               "kda_latent_decode")
+            workspace = _decode_workspace(s, cs, dev)
+        return lib.kda_latent_decode(q_p, cache.data_ptr(), table_p, lens_p, mask_p,
+                                     out.data_ptr(), lse_p, ctypes.byref(s), ctypes.byref(cs),
+                                     workspace.data_ptr(), workspace.numel(), status_p, st)
+
+    _check(_launch(dev, stream, call), "kda_latent_decode")
     return out
 
 
