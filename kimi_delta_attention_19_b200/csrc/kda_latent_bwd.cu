@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *full = bar, *empty = bar + 3, *res_full = bar + 6, *s_full = bar + 7, *dp_full = bar + 8,
            *s_read = bar + 9, *p_ready = bar + 10, *ds_ready = bar + 11, *p_free = bar + 12,
            *ds_free = bar + 13, *o_full = bar + 14, *v_full = bar + 15, *v_empty = bar + 16,
-           *drain = bar + 17;
+           *drain = bar + 17, *last = bar + 18, *fixed = bar + 19;
   uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + kTm);
   volatile int* bail = reinterpret_cast<volatile int*>(sm + kBail);
   const uint32_t sb = smem_u32(sm);
@@ -135,6 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(v_full, 1);
     mbar_init(v_empty, 1);
     mbar_init(drain, 1);
+    mbar_init(last, 1);
+    mbar_init(fixed, 32);
     fence_mbar_init();
     *bail = 0;
   }
@@ -179,79 +181,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t i64 = idesc_bf16(BM, BQ, 0, 0), iv = idesc_bf16(BM, 128, 0, 1),
                          ik = idesc_bf16(BM, 192, 0, 1);
       auto stage = [&](int t) { return sb + SmK::ST + t % kQStages * SmK::STAGE; };
+      const uint64_t k0 = sdesc_sw128(sb + SmK::K, 16, 1024), v0 = sdesc_sw128(sb + SmK::V, 16, 1024);
       auto scores = [&](int t) {  // S^T = K Q^T
         wait_for(full + t % kQStages, t / kQStages & 1, bail);
-        const int valid = r.lq - (j0 + t) * BQ;
-        if (valid < BQ) {  // rows past the sequence may hold anything: 0 x NaN is NaN
-          zero_rows(sm + SmK::ST + t % kQStages * SmK::STAGE, kAtomQ, 5, valid, BQ, lane);
-          fence_async_smem();
-          __syncwarp();
+        if (r.lq - (j0 + t) * BQ < BQ) {
+          mbar_arrive(last);
+          wait_for(fixed, 0, bail);
         }
-        const bool dead = bailed(bail);
         tc_fence_after();
-        if (elect_one() && !dead) {
+        const uint64_t qb = sdesc_sw128(stage(t), 16, 1024);
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const uint64_t ka = sdesc_sw128(sb + SmK::K + i * kAtom, 16, 1024);
-            const uint64_t qb = sdesc_sw128(stage(t) + i * kAtomQ, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(tb + S, ka + 2 * k, qb + 2 * k, i64, i > 0 || k > 0);
-          }
-          umma_commit(s_full);
-        }
-        __syncwarp();
+        for (int k = 0; k < 12; ++k)
+          umma_bf16(tb + S, k0 + k / 4 * (kAtom / 16) + k % 4 * 2,
+                    qb + k / 4 * (kAtomQ / 16) + k % 4 * 2, i64, k > 0);
+        umma_commit(s_full);
       };
       auto dprobs = [&](int t) {  // dP^T = V dO^T
-        const bool dead = bailed(bail);
-        if (elect_one() && !dead) {
+        const uint64_t gb = sdesc_sw128(stage(t) + 3 * kAtomQ, 16, 1024);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint64_t va = sdesc_sw128(sb + SmK::V + i * kAtom, 16, 1024);
-            const uint64_t gb = sdesc_sw128(stage(t) + (3 + i) * kAtomQ, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(tb + DP, va + 2 * k, gb + 2 * k, i64, i > 0 || k > 0);
-          }
-          umma_commit(dp_full);
-        }
-        __syncwarp();
+        for (int k = 0; k < 8; ++k)
+          umma_bf16(tb + DP, v0 + k / 4 * (kAtom / 16) + k % 4 * 2,
+                    gb + k / 4 * (kAtomQ / 16) + k % 4 * 2, i64, k > 0);
+        umma_commit(dp_full);
       };
-      wait_for(res_full, 0, bail);
-      scores(0);
-      dprobs(0);
-      for (int t = 0; t < n; ++t) {
-        wait_for(s_read, t & 1, bail);
-        if (t + 1 < n) scores(t + 1);
-        wait_for(p_ready, t & 1, bail);
-        bool dead = bailed(bail);
-        tc_fence_after();
-        if (elect_one() && !dead) {
+      if (elect_one()) {
+        wait_for(res_full, 0, bail);
+        scores(0);
+        dprobs(0);
+        for (int t = 0; t < n; ++t) {
+          wait_for(s_read, t & 1, bail);
+          if (t + 1 < n) scores(t + 1);
+          wait_for(p_ready, t & 1, bail);
+          tc_fence_after();
           const uint64_t gb = sdesc_sw128(stage(t) + 3 * kAtomQ, kAtomQ, 1024);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_bf16_tmem_a(tb + DVC, tb + P + 8 * k, gb + 128 * k, iv, t > 0 || k > 0);
           umma_commit(p_free);
-        }
-        __syncwarp();
-        wait_for(ds_ready, t & 1, bail);
-        tc_fence_after();
-        if (t + 1 < n) dprobs(t + 1);
-        dead = bailed(bail);
-        if (elect_one() && !dead) {
+          wait_for(ds_ready, t & 1, bail);
+          tc_fence_after();
+          if (t + 1 < n) dprobs(t + 1);
           const uint64_t qb = sdesc_sw128(stage(t), kAtomQ, 1024);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_bf16_tmem_a(tb + DK, tb + DS + 8 * k, qb + 128 * k, ik, t > 0 || k > 0);
           umma_commit(ds_free);
           umma_commit(empty + t % kQStages);
-          if (t + 1 == n) umma_commit(o_full);
         }
-        __syncwarp();
+        umma_commit(o_full);
+        if (*bail) {
+          umma_commit(drain);
+          mbar_wait(drain, 0, 20000000LL);
+        }
       }
-      if (bailed(bail)) {
-        if (elect_one()) umma_commit(drain);
-        __syncwarp();
-        mbar_wait(drain, 0, 20000000LL);
-      }
+    } else if (warp == 2 && n > 0 && r.lq - (j1 - 1) * BQ < BQ) {
+      // queries past the sequence may hold anything (0 x NaN is NaN): cleared
+      wait_for(last, 0, bail);
+      zero_rows(sm + SmK::ST + (n - 1) % kQStages * SmK::STAGE, kAtomQ, 5, r.lq - (j1 - 1) * BQ, BQ, lane);
+      fence_async_smem();
+      mbar_arrive(fixed);
     } else if (warp >= 4) {
       const int g = (warp - 4) / 4, w = warp % 4;
       const uint32_t lanes = tb + (static_cast<uint32_t>(w * 32) << 16);
@@ -383,71 +371,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1 && n > 0) {
       constexpr uint32_t i128 = idesc_bf16(BM, BM, 0, 0), iq = idesc_bf16(BM, 192, 0, 1);
+      const uint64_t q0 = sdesc_sw128(sb + SmQ::Q, 16, 1024), g0 = sdesc_sw128(sb + SmQ::DO, 16, 1024),
+                     v0 = sdesc_sw128(sb + SmQ::V, 16, 1024);
+      auto keys = [&](int t, uint32_t lbo) {
+        return sdesc_sw128(sb + SmQ::K + (t & 1) * 3 * kAtom, lbo, 1024);
+      };
       auto scores = [&](int t) {  // S = Q K^T
         wait_for(full + (t & 1), t / 2 & 1, bail);
-        const bool dead = bailed(bail);
         tc_fence_after();
-        if (elect_one() && !dead) {
+        const uint64_t kb = keys(t, 16);
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const uint64_t qa = sdesc_sw128(sb + SmQ::Q + i * kAtom, 16, 1024);
-            const uint64_t kb = sdesc_sw128(sb + SmQ::K + ((t & 1) * 3 + i) * kAtom, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(tb + S, qa + 2 * k, kb + 2 * k, i128, i > 0 || k > 0);
-          }
-          umma_commit(s_full);
+        for (int k = 0; k < 12; ++k) {
+          const int at = k / 4 * (kAtom / 16) + k % 4 * 2;
+          umma_bf16(tb + S, q0 + at, kb + at, i128, k > 0);
         }
-        __syncwarp();
+        umma_commit(s_full);
       };
       auto dprobs = [&](int t) {  // dP = dO V^T
         wait_for(v_full, t & 1, bail);
-        const bool dead = bailed(bail);
         tc_fence_after();
-        if (elect_one() && !dead) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint64_t ga = sdesc_sw128(sb + SmQ::DO + i * kAtom, 16, 1024);
-            const uint64_t vb = sdesc_sw128(sb + SmQ::V + i * kAtom, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(tb + DP, ga + 2 * k, vb + 2 * k, i128, i > 0 || k > 0);
-          }
-          umma_commit(dp_full);
-          umma_commit(v_empty);
+        for (int k = 0; k < 8; ++k) {
+          const int at = k / 4 * (kAtom / 16) + k % 4 * 2;
+          umma_bf16(tb + DP, g0 + at, v0 + at, i128, k > 0);
         }
-        __syncwarp();
+        umma_commit(dp_full);
+        umma_commit(v_empty);
       };
-      wait_for(res_full, 0, bail);
-      scores(0);
-      dprobs(0);
-      for (int t = 0; t < n; ++t) {
-        wait_for(s_read, t & 1, bail);
-        if (t + 1 < n) scores(t + 1);
-        wait_for(ds_ready, t & 1, bail);
-        tc_fence_after();
-        if (t + 1 < n) dprobs(t + 1);
-        const int valid = r.lk - t * BM;
-        if (valid < BM) {  // rows past the sequence may hold anything: 0 x NaN is NaN
-          zero_rows(sm + SmQ::K + (t & 1) * 3 * kAtom, kAtom, 3, valid, BM, lane);
-          fence_async_smem();
-          __syncwarp();
-        }
-        const bool dead = bailed(bail);
-        if (elect_one() && !dead) {
-          const uint64_t kb = sdesc_sw128(sb + SmQ::K + (t & 1) * 3 * kAtom, kAtom, 1024);
+      if (elect_one()) {
+        wait_for(res_full, 0, bail);
+        scores(0);
+        dprobs(0);
+        for (int t = 0; t < n; ++t) {
+          wait_for(s_read, t & 1, bail);
+          if (t + 1 < n) scores(t + 1);
+          wait_for(ds_ready, t & 1, bail);
+          tc_fence_after();
+          if (t + 1 < n) dprobs(t + 1);
+          if (r.lk - t * BM < BM) {
+            mbar_arrive(last);
+            wait_for(fixed, 0, bail);
+          }
+          const uint64_t kb = keys(t, kAtom);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             umma_bf16_tmem_a(tb + DQ, tb + DS + 8 * k, kb + 128 * k, iq, t > 0 || k > 0);
           umma_commit(ds_free);
           umma_commit(empty + (t & 1));
-          if (t + 1 == n) umma_commit(o_full);
         }
-        __syncwarp();
+        umma_commit(o_full);
+        if (*bail) {
+          umma_commit(drain);
+          mbar_wait(drain, 0, 20000000LL);
+        }
       }
-      if (bailed(bail)) {
-        if (elect_one()) umma_commit(drain);
-        __syncwarp();
-        mbar_wait(drain, 0, 20000000LL);
-      }
+    } else if (warp == 2 && n > 0 && r.lk - (n - 1) * BM < BM) {
+      // keys past the sequence may hold anything (0 x NaN is NaN): cleared once S is formed
+      wait_for(last, 0, bail);
+      zero_rows(sm + SmQ::K + ((n - 1) & 1) * 3 * kAtom, kAtom, 3, r.lk - (n - 1) * BM, BM, lane);
+      fence_async_smem();
+      mbar_arrive(fixed);
     } else if (warp >= 4) {
       const int g = (warp - 4) / 4, w = warp % 4;  // g: half of the keys of a step
       const uint32_t lanes = tb + (static_cast<uint32_t>(w * 32) << 16);

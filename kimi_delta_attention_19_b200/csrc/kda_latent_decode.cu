@@ -20,8 +20,8 @@
 // on the host: lengths may change under a captured graph.
 //
 // Warps: 0 loads (TMA boxes of a page's rows, 64 channels wide; two 74 KB stages, each in
-// five groups that are loaded and released separately), 1 issues the products (whichever of
-// the next tile's S^T or this tile's O^T is ready), 4-7 softmax and results; with an 8-bit
+// five groups that are loaded and released separately), 1 issues S^T, 2 O^T, 4-7 softmax and
+// results; with an 8-bit
 // cache warps 8-15 read the codes and write them as bf16 (exact) into the stage.
 #include "kda_latent_tc.cuh"
 
@@ -35,12 +35,13 @@ constexpr uint32_t kAtom = KT * 128;      // bytes of one
 constexpr uint32_t kStage = kAtoms * kAtom;
 constexpr int kGroups = 5;                // column groups loaded together: 4 x 128 channels, k_pe
 constexpr int kMaxCtas = 160;             // of the workspace; the grid is at most this
+constexpr int kAhead = 4;                 // tiles the L2 is warmed ahead of the copies
 constexpr float kRaise = 8.f;             // log2 units a score may pass its column's reference
 
 template <int NC>
 struct Sm {
   static constexpr uint32_t X = 0, Q = 2 * kStage, P = Q + kAtoms * NC * 128,
-                            BAR = P + KT * 128, TM = BAR + 28 * 8, BAIL = TM + 4, BADT = BAIL + 4,
+                            BAR = P + KT * 128, TM = BAR + 32 * 8, BAIL = TM + 4, BADT = BAIL + 4,
                             WORDS = BADT + 24, RED = WORDS + NC * 8, FAC = RED + 4 * NC * 4,
                             START = FAC + NC * 4, BYTES = START + 64;
 };
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR);
   uint64_t *full = bar, *empty = bar + 10, *s_full = bar + 20, *p_full = bar + 22,
            *pv_done = bar + 23, *q_full = bar + 24, *q_empty = bar + 25, *o_free = bar + 26,
-           *drain = bar + 27;
+           *s_read = bar + 27, *drain = bar + 29;
   uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + S::TM);
   volatile int* bail = reinterpret_cast<volatile int*>(sm + S::BAIL);
   volatile int* bad_tile = reinterpret_cast<volatile int*>(sm + S::BADT);
@@ -170,7 +171,10 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(o_free, 128);
-    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_read + i, 128);
+      mbar_init(drain + i, 1);
+    }
     fence_mbar_init();
     *bail = 0;
     bad_tile[0] = bad_tile[1] = 0;
@@ -249,6 +253,28 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
     // ------------------------------------------------------------------ loads
     const int ps = d.c.page_size, pr = ps < KT ? ps : KT;  // rows of a box
     int t = 0, q_loads = 0;
+    // The L2 is warmed kAhead tiles ahead with a page's rows in one piece: the boxes are 128
+    // bytes of each row, which DRAM by itself serves at little more than half its rate.
+    Walk pf = wk;
+    int pi = 0;
+    pf.cnt = 0;
+    auto prefetch = [&] {
+      if (pi == pf.cnt) {
+        if (!pf.next(a)) {
+          pf.cnt = pi = 0;
+          return;
+        }
+        pi = 0;
+      }
+      const int pos = (pf.st + pi++) * KT + lane * pr;
+      if (lane < KT / pr && pos < pf.len) {
+        const int64_t page = d.table[pf.sn * d.table_pages + pos / ps];
+        const uint32_t row = F8 ? kRow8 : DX * 2;
+        if (page >= 0 && page < d.c.n_pages)
+          bulk_prefetch_l2(d.c.cache + (page * ps + pos % ps) * row, pr * row);
+      }
+    };
+    for (int k = 0; k < kAhead; ++k) prefetch();
     for (int seg = 0; wk.next(a); ++seg) {
       auto load_q = [&] {
         if (seg > 0) wait_for(q_empty, (seg - 1) & 1, bail);
@@ -261,8 +287,13 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
                       wk.sn * a.R + wk.srb * NC);
       };
       if (F8 || seg == 0) load_q();
-      for (int i = 0; !F8 && i < wk.cnt; ++i, ++t) {
+      for (int i = 0; i < wk.cnt; ++i, ++t) {
         const int s = t & 1;
+        prefetch();
+        if (F8) {
+          if (t >= 2) wait_for(empty + s * kGroups + 4, (t / 2 - 1) & 1, bail);
+          continue;
+        }
         const int pos = (wk.st + i) * KT + lane * pr;
         int64_t page = 0;
         const bool there = lane < KT / pr && pos < wk.len;
@@ -290,96 +321,75 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
     }
     if (bailed(bail)) {  // let the copies in flight land before the CTA ends
       if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, 20000000LL);
-      for (int k = t > 2 ? t - 2 : 0; k < t; ++k)
+      for (int k = t > 2 ? t - 2 : 0; k < t && !F8; ++k)
         for (int g = 0; g < kGroups; ++g)
           mbar_wait(full + (k & 1) * kGroups + g, k / 2 & 1, 20000000LL);
     }
   } else if (warp == 1) {
-    // --------------------------------------------------------------- products
-    constexpr uint32_t iq = idesc_bf16(64, NC, 0, 0), ip = idesc_bf16(128, NC, 1, 1);
-    Walk wp = wk;  // the segment of the next O^T product; wk: of the next S^T product
-    int qt = 0, qg = 0, qi = 0, qs = -1, pt = 0, pi = 0, pseg = -1;
-    wk.cnt = wp.cnt = 0;
-    long long last = clock64();
-    while (pt < n_tiles) {
-      bool moved = false;
-      const bool dead = bailed(bail);
-      if (qt < n_tiles && qt <= pt + 1) {  // next column group of S^T
-        if (qg == 0 && qi == wk.cnt) {     // a new segment
-          wk.next(a);
-          qi = 0;
-          ++qs;
-        }
-        const int s = qt & 1;
-        const bool ready = mbar_test(full + s * kGroups + qg, qt / 2 & 1) &&
-                           (qg > 0 || qi > 0 || mbar_test(q_full, qs & 1));
-        if (__all_sync(0xffffffffu, ready) || dead) {
-          moved = true;
-          tc_fence_after();
-          if (elect_one() && !dead) {
-            const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage + 2 * qg * kAtom, 16, 1024);
-            const uint64_t qb = sdesc_sw128(sb + S::Q + 2 * qg * NC * 128, 16, 1024);
-            const uint32_t dst = tb + 4 * NC + s * NC;
+    // --------------------------------------------------------- products: S^T
+    // Two warps issue, so that O^T of a tile waits neither for the next tile to arrive nor for
+    // its S^T to be issued (~30 clocks an instruction).
+    constexpr uint32_t iq = idesc_bf16(64, NC, 0, 0);
+    if (elect_one()) {
+      int t = 0;
+      for (int seg = 0; wk.next(a); ++seg) {
+        wait_for(q_full, seg & 1, bail);
+        for (int i = 0; i < wk.cnt; ++i, ++t) {
+          const int s = t & 1;
+          const uint32_t dst = tb + 4 * NC + s * NC;
+          const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage, 16, 1024);
+          const uint64_t qb = sdesc_sw128(sb + S::Q, 16, 1024);
+          if (t >= 2) wait_for(s_read + s, (t / 2 - 1) & 1, bail);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) umma_bf16(dst, xa + 2 * k, qb + 2 * k, iq, qg > 0 || k > 0);
-            if (qg < 4) {
+          for (int g = 0; g < kGroups; ++g) {
+            wait_for(full + s * kGroups + g, t / 2 & 1, bail);
+            tc_fence_after();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_bf16(dst, xa + kAtom / 16 + 2 * k, qb + NC * 8 + 2 * k, iq, 1);
-            } else {
-              umma_commit(s_full + s);
-              umma_commit(empty + s * kGroups + 4);
-              if (qi + 1 == wk.cnt) umma_commit(q_empty);
+            for (int k = 0; k < (g < 4 ? 8 : 4); ++k) {
+              const int at = 2 * g + k / 4;  // column group
+              umma_bf16(dst, xa + at * (kAtom / 16) + k % 4 * 2, qb + at * (NC * 8) + k % 4 * 2, iq,
+                        g > 0 || k > 0);
             }
           }
-          __syncwarp();
-          if (++qg == kGroups) {
-            qg = 0;
-            ++qi;
-            ++qt;
-          }
+          umma_commit(s_full + s);
+          umma_commit(empty + s * kGroups + 4);
+          if (i + 1 == wk.cnt) umma_commit(q_empty);
         }
       }
-      if (pt < qt) {  // O^T of the tile whose P is ready
-        const bool first = pi == wp.cnt;
-        const bool ready = mbar_test(p_full, pt & 1) &&
-                           (!first || pseg < 0 || mbar_test(o_free, pseg & 1));
-        if (__all_sync(0xffffffffu, ready) || dead) {
-          moved = true;
-          if (first) {
-            wp.next(a);
-            pi = 0;
-            ++pseg;
-          }
-          tc_fence_after();
-          if (elect_one() && !dead) {
-            const int s = pt & 1;
-            const uint64_t pb = sdesc_sw128(sb + S::P, 8192, 1024);
-#pragma unroll
-            for (int mb = 0; mb < 4; ++mb) {
-              const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage + 2 * mb * kAtom, kAtom, 1024);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_bf16(tb + mb * NC, xa + 128 * k, pb + 128 * k, ip, pi > 0 || k > 0);
-              umma_commit(empty + s * kGroups + mb);
-            }
-            umma_commit(pv_done);
-          }
-          __syncwarp();
-          ++pi;
-          ++pt;
-        }
-      }
-      if (moved) {
-        last = clock64();
-      } else if (clock64() - last > kWaitCycles) {
-        *bail = 1;
+      if (*bail) {
+        umma_commit(drain);
+        mbar_wait(drain, 0, 20000000LL);
       }
     }
-    if (bailed(bail)) {
-      if (elect_one()) umma_commit(drain);
-      __syncwarp();
-      mbar_wait(drain, 0, 20000000LL);
+  } else if (warp == 2) {
+    // --------------------------------------------------------- products: O^T
+    constexpr uint32_t ip = idesc_bf16(128, NC, 1, 1);
+    if (elect_one()) {
+      int t = 0;
+      for (int seg = 0; wk.next(a); ++seg) {
+        for (int i = 0; i < wk.cnt; ++i, ++t) {
+          const int s = t & 1;
+          const uint64_t pb = sdesc_sw128(sb + S::P, 8192, 1024);
+          const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage, kAtom, 1024);
+          for (int g = 0; g < 4; ++g) wait_for(full + s * kGroups + g, t / 2 & 1, bail);
+          wait_for(p_full, t & 1, bail);
+          if (i == 0 && seg > 0) wait_for(o_free, (seg - 1) & 1, bail);
+          tc_fence_after();
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_bf16(tb + mb * NC, xa + 2 * mb * (kAtom / 16) + 128 * k, pb + 128 * k, ip,
+                        i > 0 || k > 0);
+            umma_commit(empty + s * kGroups + mb);
+          }
+          umma_commit(pv_done);
+        }
+      }
+      if (*bail) {
+        umma_commit(drain + 1);
+        mbar_wait(drain + 1, 0, 20000000LL);
+      }
     }
   } else if (warp >= 4 && warp < 8) {
     // ---------------------------------------------------- softmax and results
@@ -448,6 +458,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
             }
           }
         }
+        tc_fence_before();
+        mbar_arrive(s_read + s);
         const int kj = (wk.st + i) * KT + kk - first;  // among the query tokens
         if (kk >= valid) {
 #pragma unroll

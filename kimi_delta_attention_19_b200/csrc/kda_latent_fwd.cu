@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(384, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Sm::BAR);
   uint64_t *full = bar, *empty = bar + 8, *q_full = bar + 16, *s_full = bar + 18,
-           *p_full = bar + 20, *o_full = bar + 22, *drain = bar + 24;
+           *p_full = bar + 20, *o_full = bar + 22, *drain = bar + 24, *v_last = bar + 25, *v_fixed = bar + 26;
   uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + Sm::TM);
   volatile int* bail = reinterpret_cast<volatile int*>(sm + Sm::BAIL);
   const uint32_t sb = smem_u32(sm);
@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(o_full + g, 1);
     }
     mbar_init(drain, 1);
+    mbar_init(v_last, 1);
+    mbar_init(v_fixed, 32);
     fence_mbar_init();
     *bail = 0;
   }
@@ -130,6 +132,7 @@ __global__ void __launch_bounds__(384, 1)
       // ------------------------------------------------------------- products
       constexpr uint32_t iq = idesc_bf16(BM, BN, 0, 0), iv = idesc_bf16(BM, 128, 0, 1),
                          ih = idesc_bf16(BM, 64, 0, 1);
+      const uint64_t q0 = sdesc_sw128(sb + Sm::Q, 16, 1024);
       auto ring = [&](int c) { return sb + Sm::RING + c % kRing * kAtom; };
       auto wait_group = [&](int c) { wait_for(full + c % kRing, c / kRing & 1, bail); };
       auto qk = [&](int g, int j, bool release) {
@@ -138,75 +141,70 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 3; ++i) {
           const int c = kPerTile * j + i;
           wait_group(c);
-          const bool dead = bailed(bail);
           tc_fence_after();
-          if (elect_one() && !dead) {
-            const uint64_t qa = sdesc_sw128(sb + Sm::Q + (3 * g + i) * kAtom, 16, 1024);
-            const uint64_t kb = sdesc_sw128(ring(c), 16, 1024);
+          const uint64_t qa = q0 + (3 * g + i) * (kAtom / 16), kb = sdesc_sw128(ring(c), 16, 1024);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16(tb + g * BN, qa + 2 * k, kb + 2 * k, iq, i > 0 || k > 0);
-            if (release) umma_commit(empty + c % kRing);
-            if (i == 2) umma_commit(s_full + g);
-          }
-          __syncwarp();
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tb + g * BN, qa + 2 * k, kb + 2 * k, iq, i > 0 || k > 0);
+          if (release) umma_commit(empty + c % kRing);
         }
+        umma_commit(s_full + g);
       };
       auto pv = [&](int g, int j, bool release) {
         const int c = kPerTile * j + 3;
         wait_group(c);
         wait_group(c + 1);
-        const int valid = r.lk - j * BN;
-        if (valid < BN && (g == 0 || j >= nk[0])) {
-          // rows past the sequence may hold anything: 0 x NaN is NaN
-          for (int e = lane; e < (BN - valid) * 16; e += 32)
-            *reinterpret_cast<uint4*>(sm + Sm::RING + (c + (e >> 3 & 1)) % kRing * kAtom +
-                                      sw128_chunk(valid + (e >> 4), e & 7, 0)) =
-                make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-          __syncwarp();
+        if (r.lk - j * BN < BN) {
+          if (g == 0 || j >= nk[0]) mbar_arrive(v_last);
+          wait_for(v_fixed, 0, bail);
         }
         wait_for(p_full + g, j & 1, bail);
-        const bool dead = bailed(bail);
         tc_fence_after();
-        if (elect_one() && !dead) {
-          const uint32_t o = tb + 256 + g * 128, p = tb + g * BN;
-          if (c % kRing != kRing - 1) {
-            const uint64_t vb = sdesc_sw128(ring(c), kAtom, 1024);
+        const uint32_t o = tb + 256 + g * 128, p = tb + g * BN;
+        if (c % kRing != kRing - 1) {
+          const uint64_t vb = sdesc_sw128(ring(c), kAtom, 1024);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_tmem_a(o, p + 8 * k, vb + 128 * k, iv, j > 0 || k > 0);
+        } else {  // the ring's end between v's two column groups
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t vb = sdesc_sw128(ring(c + i), kAtom, 1024);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              umma_bf16_tmem_a(o, p + 8 * k, vb + 128 * k, iv, j > 0 || k > 0);
-          } else {  // the ring's end between v's two column groups
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint64_t vb = sdesc_sw128(ring(c + i), kAtom, 1024);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                umma_bf16_tmem_a(o + 64 * i, p + 8 * k, vb + 128 * k, ih, j > 0 || k > 0);
-            }
+              umma_bf16_tmem_a(o + 64 * i, p + 8 * k, vb + 128 * k, ih, j > 0 || k > 0);
           }
-          if (release) {
-            umma_commit(empty + c % kRing);
-            umma_commit(empty + (c + 1) % kRing);
-          }
-          if (j + 1 == nk[g]) umma_commit(o_full + g);
         }
-        __syncwarp();
+        if (release) {
+          umma_commit(empty + c % kRing);
+          umma_commit(empty + (c + 1) % kRing);
+        }
+        if (j + 1 == nk[g]) umma_commit(o_full + g);
       };
-      if (nk[0] > 0) qk(0, 0, nk[1] == 0);
-      if (nk[1] > 0) qk(1, 0, true);
-      for (int j = 0; j < n; ++j) {
+      if (elect_one()) {
+        if (nk[0] > 0) qk(0, 0, nk[1] == 0);
+        if (nk[1] > 0) qk(1, 0, true);
+        for (int j = 0; j < n; ++j) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (j < nk[g]) pv(g, j, g == 1 || j >= nk[1]);
-          if (j + 1 < nk[g]) qk(g, j + 1, g == 1 || j + 1 >= nk[1]);
+          for (int g = 0; g < 2; ++g) {
+            if (j < nk[g]) pv(g, j, g == 1 || j >= nk[1]);
+            if (j + 1 < nk[g]) qk(g, j + 1, g == 1 || j + 1 >= nk[1]);
+          }
+        }
+        if (*bail) {
+          umma_commit(drain);
+          mbar_wait(drain, 0, 20000000LL);
         }
       }
-      if (bailed(bail)) {
-        if (elect_one()) umma_commit(drain);
-        __syncwarp();
-        mbar_wait(drain, 0, 20000000LL);
-      }
+    } else if (warp == 2 && n > 0 && r.lk - (n - 1) * BN < BN) {
+      // v's rows past the sequence may hold anything (0 x NaN is NaN): cleared
+      const int c = kPerTile * (n - 1) + 3, valid = r.lk - (n - 1) * BN;
+      wait_for(v_last, 0, bail);
+      for (int e = lane; e < (BN - valid) * 16; e += 32)
+        *reinterpret_cast<uint4*>(sm + Sm::RING + (c + (e >> 3 & 1)) % kRing * kAtom +
+                                  sw128_chunk(valid + (e >> 4), e & 7, 0)) = make_uint4(0, 0, 0, 0);
+      fence_async_smem();
+      mbar_arrive(v_fixed);
     }
   } else {
     // -------------------------------------------------------- softmax, results

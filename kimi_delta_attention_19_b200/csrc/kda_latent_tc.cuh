@@ -13,9 +13,9 @@ namespace latent {
 
 using namespace sm100;
 
-// One thread of a converged warp, the same one each time. A branch on it is known to be
-// uniform, so tcgen05.mma issues every ~25 clocks; under `lane == 0` each one took ~97
-// (measured, M = 128, N = 32, 512 in a row): more than the instruction itself.
+// One thread of a converged warp, the same one each time. It runs an issuing role by itself:
+// under a branch on it tcgen05.mma goes out every ~30 clocks, under one on `lane == 0` every ~97
+// (measured, M = 128, N = 32, 512 in a row), which is more than the instruction takes.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -36,9 +36,9 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 }
 
 // Bounded waits. `bail` is a shared word of the CTA: the first wait that runs out (about a
-// second) sets it, every later wait returns at once, no further copy or product is issued,
-// and all loops run to their ends (so no named barrier is left short); the kernel then waits
-// for what it has in flight, reports kDevWaitTimeout and frees its tensor memory.
+// second) sets it, every later wait returns at once, no further copy is issued, and all loops
+// run to their ends (so no named barrier is left short); the kernel then waits for what it has
+// in flight, reports kDevWaitTimeout and frees its tensor memory.
 constexpr long long kWaitCycles = 2000000000LL;
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* bail) {
   if (mbar_try_wait(bar, parity)) return;
