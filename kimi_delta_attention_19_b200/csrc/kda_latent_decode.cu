@@ -35,7 +35,6 @@ constexpr uint32_t kAtom = KT * 128;      // bytes of one
 constexpr uint32_t kStage = kAtoms * kAtom;
 constexpr int kGroups = 5;                // column groups loaded together: 4 x 128 channels, k_pe
 constexpr int kMaxCtas = 160;             // of the workspace; the grid is at most this
-constexpr int kAhead = 4;                 // tiles the L2 is warmed ahead of the copies
 constexpr float kRaise = 8.f;             // log2 units a score may pass its column's reference
 
 template <int NC>
@@ -109,25 +108,40 @@ struct Walk {
   }
 };
 
-// four e4m3 codes as bf16 times 2^e: the code's bits in a bf16's place read as its value times
-// 2^-120, so two exact products (2^120, then 2^e in both halves of `sc`) give the value
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint2 values4(uint32_t w, uint32_t sc) {
-  uint32_t lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);  // codes in upper bytes
-  lo = (lo & 0x80008000u) | (lo >> 4 & 0x07f007f0u);
-  hi = (hi & 0x80008000u) | (hi >> 4 & 0x07f007f0u);
-  uint2 r = make_uint2(mul2(mul2(lo, 0x7b807b80u), sc), mul2(mul2(hi, 0x7b807b80u), sc));
-  if (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // a NaN among them
-    if ((w & 0x7fu) == 0x7fu) r.x |= 0x7fffu;
-    if ((w & 0x7f00u) == 0x7f00u) r.x |= 0x7fff0000u;
-    if ((w & 0x7f0000u) == 0x7f0000u) r.y |= 0x7fffu;
-    if ((w & 0x7f000000u) == 0x7f000000u) r.y |= 0x7fff0000u;
+// Eight e4m3 codes' words as bf16 pairs times 2^e, exactly. A code's bits in a bf16's place read
+// as its value times 2^-120, so the value is that times 2^(120 + e): one product where the
+// factor is a bf16 number (`be` = e + 127 <= 134), else two.
+__device__ __forceinline__ void values16(const uint4& code, uint32_t be, uint32_t (&v)[8]) {
+  const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+  uint32_t nan = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = __byte_perm(w[k], 0, 0x1404), hi = __byte_perm(w[k], 0, 0x3424);
+    v[2 * k] = (lo & 0x80008000u) | (lo >> 4 & 0x07f007f0u);  // codes were in the upper bytes
+    v[2 * k + 1] = (hi & 0x80008000u) | (hi >> 4 & 0x07f007f0u);
+    nan |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
   }
-  return r;
+  if (be <= 134) {
+    const uint32_t f = (be + 120) * 0x00800080u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = mul2(mul2(v[k], 0x7b807b80u), be * 0x00800080u);
+  }
+  if (nan & 0x80808080u) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t c = w[k / 2] >> (16 * (k & 1));
+      if ((c & 0x7fu) == 0x7fu) v[k] |= 0x7fffu;
+      if ((c & 0x7f00u) == 0x7f00u) v[k] |= 0x7fff0000u;
+    }
+  }
 }
 
 template <int NC, bool F8>
@@ -249,149 +263,127 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
   wk.tile = wk.left > 0 ? static_cast<int>(start[2]) : 0;
   const int n_tiles = wk.left;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ loads
-    const int ps = d.c.page_size, pr = ps < KT ? ps : KT;  // rows of a box
-    int t = 0, q_loads = 0;
-    // The L2 is warmed kAhead tiles ahead with a page's rows in one piece: the boxes are 128
-    // bytes of each row, which DRAM by itself serves at little more than half its rate.
-    Walk pf = wk;
-    int pi = 0;
-    pf.cnt = 0;
-    auto prefetch = [&] {
-      if (pi == pf.cnt) {
-        if (!pf.next(a)) {
-          pf.cnt = pi = 0;
-          return;
-        }
-        pi = 0;
-      }
-      const int pos = (pf.st + pi++) * KT + lane * pr;
-      if (lane < KT / pr && pos < pf.len) {
-        const int64_t page = d.table[pf.sn * d.table_pages + pos / ps];
-        const uint32_t row = F8 ? kRow8 : DX * 2;
-        if (page >= 0 && page < d.c.n_pages)
-          bulk_prefetch_l2(d.c.cache + (page * ps + pos % ps) * row, pr * row);
-      }
-    };
-    for (int k = 0; k < kAhead; ++k) prefetch();
-    for (int seg = 0; wk.next(a); ++seg) {
-      auto load_q = [&] {
-        if (seg > 0) wait_for(q_empty, (seg - 1) & 1, bail);
-        if (bailed(bail)) return;
-        ++q_loads;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, kAtoms * NC * 128);
-        __syncwarp();
-        if (lane < kAtoms)
-          tma_load_2d(sm + S::Q + lane * NC * 128, &maps.q, q_full, lane * 64,
-                      wk.sn * a.R + wk.srb * NC);
-      };
-      if (F8 || seg == 0) load_q();
-      for (int i = 0; i < wk.cnt; ++i, ++t) {
-        const int s = t & 1;
-        prefetch();
-        if (F8) {
-          if (t >= 2) wait_for(empty + s * kGroups + 4, (t / 2 - 1) & 1, bail);
-          continue;
-        }
-        const int pos = (wk.st + i) * KT + lane * pr;
-        int64_t page = 0;
-        const bool there = lane < KT / pr && pos < wk.len;
-        if (there) page = d.table[wk.sn * d.table_pages + pos / ps];
-        const bool bad = page < 0 || page >= d.c.n_pages;
-        if (bad) page = 0;
-        if (__any_sync(0xffffffffu, bad) && lane == 0) bad_tile[s] = t + 1;
-        const int nb = __popc(__ballot_sync(0xffffffffu, there));
-        const int row = static_cast<int>(page * ps + pos % ps);
-        const int y = __shfl_sync(0xffffffffu, row, lane >> 1 & 3);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
-          if (bailed(bail)) continue;
-          uint64_t* f = full + s * kGroups + g;
-          if (lane == 0) mbar_arrive_expect_tx(f, nb * pr * (g < 4 ? 256 : 128));
+  // registers: 80 + 176 + 2 x 128 a thread of the four warpgroups of an 8-bit launch
+  if (warp < 4) {
+    if constexpr (F8) reg_dec<80>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------ loads
+      const int ps = d.c.page_size, pr = ps < KT ? ps : KT;  // rows of a box
+      int t = 0, q_loads = 0;
+      for (int seg = 0; wk.next(a); ++seg) {
+        auto load_q = [&] {
+          if (seg > 0) wait_for(q_empty, (seg - 1) & 1, bail);
+          if (bailed(bail)) return;
+          ++q_loads;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, kAtoms * NC * 128);
           __syncwarp();
-          const int atom = 2 * g + (lane & 1);
-          if (lane < 2 * nb && atom < kAtoms)
-            tma_load_2d(sm + S::X + s * kStage + atom * kAtom + (lane >> 1) * pr * 128, &maps.x, f,
-                        atom * 64, y);
-        }
-        if (seg > 0 && i == 0) load_q();
-      }
-    }
-    if (bailed(bail)) {  // let the copies in flight land before the CTA ends
-      if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, 20000000LL);
-      for (int k = t > 2 ? t - 2 : 0; k < t && !F8; ++k)
-        for (int g = 0; g < kGroups; ++g)
-          mbar_wait(full + (k & 1) * kGroups + g, k / 2 & 1, 20000000LL);
-    }
-  } else if (warp == 1) {
-    // --------------------------------------------------------- products: S^T
-    // Two warps issue, so that O^T of a tile waits neither for the next tile to arrive nor for
-    // its S^T to be issued (~30 clocks an instruction).
-    constexpr uint32_t iq = idesc_bf16(64, NC, 0, 0);
-    if (elect_one()) {
-      int t = 0;
-      for (int seg = 0; wk.next(a); ++seg) {
-        wait_for(q_full, seg & 1, bail);
-        for (int i = 0; i < wk.cnt; ++i, ++t) {
+          if (lane < kAtoms)
+            tma_load_2d(sm + S::Q + lane * NC * 128, &maps.q, q_full, lane * 64,
+                        wk.sn * a.R + wk.srb * NC);
+        };
+        if (F8 || seg == 0) load_q();
+        for (int i = 0; !F8 && i < wk.cnt; ++i, ++t) {
           const int s = t & 1;
-          const uint32_t dst = tb + 4 * NC + s * NC;
-          const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage, 16, 1024);
-          const uint64_t qb = sdesc_sw128(sb + S::Q, 16, 1024);
-          if (t >= 2) wait_for(s_read + s, (t / 2 - 1) & 1, bail);
-#pragma unroll
+          const int pos = (wk.st + i) * KT + lane * pr;
+          int64_t page = 0;
+          const bool there = lane < KT / pr && pos < wk.len;
+          if (there) page = d.table[wk.sn * d.table_pages + pos / ps];
+          const bool bad = page < 0 || page >= d.c.n_pages;
+          if (bad) page = 0;
+          if (__any_sync(0xffffffffu, bad) && lane == 0) bad_tile[s] = t + 1;
+          const int nb = __popc(__ballot_sync(0xffffffffu, there));
+          const int row = static_cast<int>(page * ps + pos % ps);
+          const int y = __shfl_sync(0xffffffffu, row, lane >> 1 & 3);
+  #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
-            wait_for(full + s * kGroups + g, t / 2 & 1, bail);
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < (g < 4 ? 8 : 4); ++k) {
-              const int at = 2 * g + k / 4;  // column group
-              umma_bf16(dst, xa + at * (kAtom / 16) + k % 4 * 2, qb + at * (NC * 8) + k % 4 * 2, iq,
-                        g > 0 || k > 0);
+            if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
+            if (bailed(bail)) continue;
+            uint64_t* f = full + s * kGroups + g;
+            if (lane == 0) mbar_arrive_expect_tx(f, nb * pr * (g < 4 ? 256 : 128));
+            __syncwarp();
+            const int atom = 2 * g + (lane & 1);
+            if (lane < 2 * nb && atom < kAtoms)
+              tma_load_2d(sm + S::X + s * kStage + atom * kAtom + (lane >> 1) * pr * 128, &maps.x, f,
+                          atom * 64, y);
+          }
+          if (seg > 0 && i == 0) load_q();
+        }
+      }
+      if (bailed(bail)) {  // let the copies in flight land before the CTA ends
+        if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, 20000000LL);
+        for (int k = t > 2 ? t - 2 : 0; k < t && !F8; ++k)
+          for (int g = 0; g < kGroups; ++g)
+            mbar_wait(full + (k & 1) * kGroups + g, k / 2 & 1, 20000000LL);
+      }
+    } else if (warp == 1) {
+      // --------------------------------------------------------- products: S^T
+      // Two warps issue, so that O^T of a tile waits neither for the next tile to arrive nor for
+      // its S^T to be issued (~30 clocks an instruction).
+      constexpr uint32_t iq = idesc_bf16(64, NC, 0, 0);
+      if (elect_one()) {
+        int t = 0;
+        for (int seg = 0; wk.next(a); ++seg) {
+          wait_for(q_full, seg & 1, bail);
+          for (int i = 0; i < wk.cnt; ++i, ++t) {
+            const int s = t & 1;
+            const uint32_t dst = tb + 4 * NC + s * NC;
+            const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage, 16, 1024);
+            const uint64_t qb = sdesc_sw128(sb + S::Q, 16, 1024);
+            if (t >= 2) wait_for(s_read + s, (t / 2 - 1) & 1, bail);
+  #pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              wait_for(full + s * kGroups + g, t / 2 & 1, bail);
+              tc_fence_after();
+  #pragma unroll
+              for (int k = 0; k < (g < 4 ? 8 : 4); ++k) {
+                const int at = 2 * g + k / 4;  // column group
+                umma_bf16(dst, xa + at * (kAtom / 16) + k % 4 * 2, qb + at * (NC * 8) + k % 4 * 2, iq,
+                          g > 0 || k > 0);
+              }
             }
+            umma_commit(s_full + s);
+            umma_commit(empty + s * kGroups + 4);
+            if (i + 1 == wk.cnt) umma_commit(q_empty);
           }
-          umma_commit(s_full + s);
-          umma_commit(empty + s * kGroups + 4);
-          if (i + 1 == wk.cnt) umma_commit(q_empty);
+        }
+        if (*bail) {
+          umma_commit(drain);
+          mbar_wait(drain, 0, 20000000LL);
         }
       }
-      if (*bail) {
-        umma_commit(drain);
-        mbar_wait(drain, 0, 20000000LL);
-      }
-    }
-  } else if (warp == 2) {
-    // --------------------------------------------------------- products: O^T
-    constexpr uint32_t ip = idesc_bf16(128, NC, 1, 1);
-    if (elect_one()) {
-      int t = 0;
-      for (int seg = 0; wk.next(a); ++seg) {
-        for (int i = 0; i < wk.cnt; ++i, ++t) {
-          const int s = t & 1;
-          const uint64_t pb = sdesc_sw128(sb + S::P, 8192, 1024);
-          const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage, kAtom, 1024);
-          for (int g = 0; g < 4; ++g) wait_for(full + s * kGroups + g, t / 2 & 1, bail);
-          wait_for(p_full, t & 1, bail);
-          if (i == 0 && seg > 0) wait_for(o_free, (seg - 1) & 1, bail);
-          tc_fence_after();
-#pragma unroll
-          for (int mb = 0; mb < 4; ++mb) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16(tb + mb * NC, xa + 2 * mb * (kAtom / 16) + 128 * k, pb + 128 * k, ip,
-                        i > 0 || k > 0);
-            umma_commit(empty + s * kGroups + mb);
+    } else if (warp == 2) {
+      // --------------------------------------------------------- products: O^T
+      constexpr uint32_t ip = idesc_bf16(128, NC, 1, 1);
+      if (elect_one()) {
+        int t = 0;
+        for (int seg = 0; wk.next(a); ++seg) {
+          for (int i = 0; i < wk.cnt; ++i, ++t) {
+            const int s = t & 1;
+            const uint64_t pb = sdesc_sw128(sb + S::P, 8192, 1024);
+            const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage, kAtom, 1024);
+            for (int g = 0; g < 4; ++g) wait_for(full + s * kGroups + g, t / 2 & 1, bail);
+            wait_for(p_full, t & 1, bail);
+            if (i == 0 && seg > 0) wait_for(o_free, (seg - 1) & 1, bail);
+            tc_fence_after();
+  #pragma unroll
+            for (int mb = 0; mb < 4; ++mb) {
+  #pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_bf16(tb + mb * NC, xa + 2 * mb * (kAtom / 16) + 128 * k, pb + 128 * k, ip,
+                          i > 0 || k > 0);
+              umma_commit(empty + s * kGroups + mb);
+            }
+            umma_commit(pv_done);
           }
-          umma_commit(pv_done);
+        }
+        if (*bail) {
+          umma_commit(drain + 1);
+          mbar_wait(drain + 1, 0, 20000000LL);
         }
       }
-      if (*bail) {
-        umma_commit(drain + 1);
-        mbar_wait(drain + 1, 0, 20000000LL);
-      }
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < 8) {
+    if constexpr (F8) reg_inc<176>();
     // ---------------------------------------------------- softmax and results
     const int w = warp - 4, tw = tid - 128;
     const uint32_t lanes = tb + (static_cast<uint32_t>(w * 32) << 16);
@@ -616,11 +608,12 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
       gt += wk.cnt;
       group_sync(1, 128);  // fac, red and words are free
     }
-  } else if (F8 && warp >= 8) {
+  } else if (F8) {
     // ------------------------------------------- 8-bit rows, as bf16 into the stages
-    // Thread (row, quarter): 32 codes of each 128-channel group. A group's registers are
-    // refilled with the next tile's codes as soon as they are converted, so ~40 KB an SM are
-    // in flight; the block table is read a tile further ahead.
+    // Four threads a row; of each 128-channel group one takes the codes 16 q .. and 64 + 16 q ..,
+    // so that 8 threads' stores touch all banks. A group's registers are refilled with the next
+    // tile's codes as soon as they are converted, so ~40 KB an SM are in flight; the block table
+    // is read a tile further ahead.
     const int i = tid - 256, row = i / 4, qd = i % 4;
     Walk wl2 = wk;   // runs ahead
     int li = 0;
@@ -653,7 +646,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
 #pragma unroll
     for (int g = 0; g < 4; ++g)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) code[g][h] = ld(cur, g * 128 + qd * 32 + h * 16);
+      for (int h = 0; h < 2; ++h) code[g][h] = ld(cur, g * 128 + h * 64 + qd * 16);
     pe[0] = ld(cur, kPe8 + qd * 32);
     pe[1] = ld(cur, kPe8 + qd * 32 + 16);
     ex = cur.p != nullptr ? *reinterpret_cast<const uint32_t*>(cur.p + kExp8) : 0;
@@ -664,31 +657,19 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
       if (cur.bad) bad_tile[s] = t + 1;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const uint32_t e = ex >> (8 * g) & 0xffu, scale = e << 7 | e << 23;
-        uint32_t v[16];
+        uint32_t v[2][8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t wd[4] = {code[g][h].x, code[g][h].y, code[g][h].z, code[g][h].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint2 r = values4(wd[k], scale);
-            v[8 * h + 2 * k] = r.x;
-            v[8 * h + 2 * k + 1] = r.y;
-          }
-          code[g][h] = ld(nxt, g * 128 + qd * 32 + h * 16);
+          values16(code[g][h], ex >> (8 * g) & 0xffu, v[h]);
+          code[g][h] = ld(nxt, g * 128 + h * 64 + qd * 16);
         }
         if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
-        // the chunk order differs by thread, so that 8 threads' stores touch all banks
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int jj = j ^ (qd >> 1) ^ ((row & 1) << 1);
-          uint4 o;
-          o.x = jj & 2 ? (jj & 1 ? v[12] : v[8]) : (jj & 1 ? v[4] : v[0]);
-          o.y = jj & 2 ? (jj & 1 ? v[13] : v[9]) : (jj & 1 ? v[5] : v[1]);
-          o.z = jj & 2 ? (jj & 1 ? v[14] : v[10]) : (jj & 1 ? v[6] : v[2]);
-          o.w = jj & 2 ? (jj & 1 ? v[15] : v[11]) : (jj & 1 ? v[7] : v[3]);
-          *reinterpret_cast<uint4*>(xs + sw128_chunk(row, g * 16 + qd * 4 + jj, kAtom)) = o;
-        }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<uint4*>(xs + sw128_chunk(row, g * 16 + h * 8 + qd * 2 + j, kAtom)) =
+                make_uint4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full + s * kGroups + g);
