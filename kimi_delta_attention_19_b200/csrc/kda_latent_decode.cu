@@ -21,8 +21,8 @@
 //
 // Warps: 0 loads (TMA boxes of a page's rows, 64 channels wide; two 74 KB stages, each in
 // five groups that are loaded and released separately), 1 issues S^T, 2 O^T, 4-7 softmax and
-// results; with an 8-bit
-// cache warps 8-15 read the codes and write them as bf16 (exact) into the stage.
+// results (4-11 for 64 rows, 32 a warpgroup); with an 8-bit cache the warps behind them read
+// the codes and write them as bf16 (exact) into the stage.
 #include "kda_latent_tc.cuh"
 
 namespace kda {
@@ -144,14 +144,26 @@ __device__ __forceinline__ void values16(const uint4& code, uint32_t be, uint32_
   }
 }
 
+// Softmax warpgroups (up to 32 columns each), sets of eight converting warps, and registers a
+// thread: of the first warpgroup, the softmax ones and the converting ones (8-bit caches).
 template <int NC, bool F8>
-__global__ void __launch_bounds__(F8 ? 512 : 256, 1)
+struct Roles {
+  static constexpr int kSoft = NC == 64 ? 2 : 1, kSets = !F8 ? 0 : NC == 64 ? 1 : 2;
+  static constexpr int kThreads = 128 + 128 * kSoft + 256 * kSets;
+  static constexpr int kRegs = 512 / (kThreads / 128) / 8 * 8;  // at launch
+  static constexpr int kR0 = 72, kRs = NC == 64 ? 104 : 120, kRc = NC == 64 ? 96 : 72;
+  static_assert(!F8 || kR0 + kRs * kSoft + kRc * 2 * kSets <= kRegs * (kThreads / 128), "");
+};
+
+template <int NC, bool F8>
+__global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     decode_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ __align__(1024) unsigned char sm[];
   using S = Sm<NC>;
-  constexpr int NH = NC / 2;                     // rows a softmax thread holds
+  using R = Roles<NC, F8>;
+  constexpr int NW = NC / R::kSoft, NH = NW / 2;  // rows of a softmax warpgroup, of a thread
   constexpr uint32_t kCols = NC == 64 ? 512 : NC == 32 ? 256 : 128;  // 4 NC of O^T, 2 NC of S^T
-  constexpr int kThreads = F8 ? 512 : 256;
+  constexpr int kThreads = R::kThreads;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR);
   uint64_t *full = bar, *empty = bar + 10, *s_full = bar + 20, *p_full = bar + 22,
@@ -180,13 +192,13 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(s_full + 1, 1);
-    mbar_init(p_full, 128);
+    mbar_init(p_full, 128 * R::kSoft);
     mbar_init(pv_done, 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(o_free, 128);
+    mbar_init(o_free, 128 * R::kSoft);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(s_read + i, 128);
+      mbar_init(s_read + i, 128 * R::kSoft);
       mbar_init(drain + i, 1);
     }
     fence_mbar_init();
@@ -263,9 +275,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
   wk.tile = wk.left > 0 ? static_cast<int>(start[2]) : 0;
   const int n_tiles = wk.left;
 
-  // registers: 80 + 176 + 2 x 128 a thread of the four warpgroups of an 8-bit launch
   if (warp < 4) {
-    if constexpr (F8) reg_dec<80>();
+    if constexpr (F8) reg_dec<R::kR0>();
     if (warp == 0) {
       // ------------------------------------------------------------------ loads
       const int ps = d.c.page_size, pr = ps < KT ? ps : KT;  // rows of a box
@@ -382,30 +393,31 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
         }
       }
     }
-  } else if (warp < 8) {
-    if constexpr (F8) reg_inc<176>();
+  } else if (warp < 4 + 4 * R::kSoft) {
+    if constexpr (F8) reg_inc<R::kRs>();
     // ---------------------------------------------------- softmax and results
-    const int w = warp - 4, tw = tid - 128;
+    const int w = warp % 4, wg = (warp - 4) / 4, tw = tid % 128, c_lo = wg * NW;
     const uint32_t lanes = tb + (static_cast<uint32_t>(w * 32) << 16);
-    const int half = lane >> 4, ch0 = half * NH, kk = w * 16 + (lane & 15);
+    const int half = lane >> 4, ch0 = c_lo + half * NH, kk = w * 16 + (lane & 15);
     const float sl = d.scale * kLog2e;
     int t = 0;
     bool first_seg = true;
     int64_t gt = t0;  // global index of the segment's first tile
     for (; wk.next(a); first_seg = false) {
       const int first = wk.len - d.L;  // position of the first query token
-      if (tw < NC) {
-        const int row = wk.srb * NC + tw, i = row / d.H;
-        words[tw] = row >= a.R ? 0
+      if (tw < NW) {
+        const int row = wk.srb * NC + c_lo + tw, i = row / d.H;
+        words[c_lo + tw] = row >= a.R ? 0
                     : d.mask != nullptr
                         ? static_cast<uint64_t>(d.mask[static_cast<int64_t>(wk.sn) * d.L + i])
                         : (2ull << i) - 1;
       }
-      group_sync(1, 128);
-      float m[NH], l[NH];
+      group_sync(1 + wg, 128);
+      // nm: minus a column's reference in log2 units, +inf before its first score
+      float nm[NH], l[NH];
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
-        m[i] = -INFINITY;
+        nm[i] = INFINITY;
         l[i] = 0.f;
       }
       bool bad = false;
@@ -418,36 +430,15 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
         {
           // an M = 64 product's row r is in tensor-memory lane 32 (r / 16) + r % 16: the
           // upper half of a warp takes the upper half of the columns from the lower one
-          const uint32_t sc = lanes + 4 * NC + s * NC;
-          if constexpr (NC == 64) {
-            uint32_t lo[32], hi[32];
-            tmem_ld32(sc, lo);
-            tmem_ld32(sc + 32, hi);
-            tmem_ld_wait(lo);
-            tmem_ld_wait(hi);
+          const uint32_t sc = lanes + 4 * NC + s * NC + c_lo;
+          uint32_t v[NW];
+          if constexpr (NW == 32) tmem_ld32(sc, v);
+          else tmem_ld16(sc, v);
+          tmem_ld_wait(v);
 #pragma unroll
-            for (int k = 0; k < NH; ++k) {
-              const uint32_t up = __shfl_up_sync(0xffffffffu, hi[k], 16);
-              x[k] = sl * __uint_as_float(half ? up : lo[k]);
-            }
-          } else if constexpr (NC == 32) {
-            uint32_t v[32];
-            tmem_ld32(sc, v);
-            tmem_ld_wait(v);
-#pragma unroll
-            for (int k = 0; k < NH; ++k) {
-              const uint32_t up = __shfl_up_sync(0xffffffffu, v[k + NH], 16);
-              x[k] = sl * __uint_as_float(half ? up : v[k]);
-            }
-          } else {
-            uint32_t v[16];
-            tmem_ld16(sc, v);
-            tmem_ld_wait(v);
-#pragma unroll
-            for (int k = 0; k < NH; ++k) {
-              const uint32_t up = __shfl_up_sync(0xffffffffu, v[k + NH], 16);
-              x[k] = sl * __uint_as_float(half ? up : v[k]);
-            }
+          for (int k = 0; k < NH; ++k) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, v[k + NH], 16);
+            x[k] = __uint_as_float(half ? up : v[k]);
           }
         }
         tc_fence_before();
@@ -461,53 +452,61 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
           for (int k = 0; k < NH; ++k)
             if (!(words[ch0 + k] >> kj & 1)) x[k] = -INFINITY;
         }
-        bool up = false;
+        // y = log2 of p; a column without a reference gives +inf, a masked key there NaN,
+        // which the maximum passes over
+        float y[NH], top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < NH; ++k) up |= x[k] > m[k] + kRaise;
-        if (group_any(1, 128, up)) {
+        for (int k = 0; k < NH; ++k) y[k] = fmaf(x[k], sl, nm[k]);
+#pragma unroll
+        for (int k = 0; k < NH; k += 2) top = fmaxf(top, fmaxf(y[k], y[k + 1]));
+        if (group_any(1 + wg, 128, top > kRaise)) {
           // raise the columns' references to the running maximum, rescale sums and O^T
 #pragma unroll
           for (int k = 0; k < NH; ++k) {
-            float y = x[k];
+            float z = sl * x[k];
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1)
-              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-            if ((lane & 15) == 0) red[w * NC + ch0 + k] = y;
+              z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, off));
+            if ((lane & 15) == 0) red[w * NC + ch0 + k] = z;
           }
-          group_sync(1, 128);
+          group_sync(1 + wg, 128);
 #pragma unroll
           for (int k = 0; k < NH; ++k) {
             const int cc = ch0 + k;
-            const float y = fmaxf(fmaxf(red[cc], red[NC + cc]), fmaxf(red[2 * NC + cc], red[3 * NC + cc]));
-            const float mn = fmaxf(m[k], y);
-            const float f = m[k] == -INFINITY ? 0.f : ex2(m[k] - mn);
+            const float z = fmaxf(fmaxf(red[cc], red[NC + cc]), fmaxf(red[2 * NC + cc], red[3 * NC + cc]));
+            const float mn = -fmaxf(-nm[k], z);
+            const float f = nm[k] == INFINITY ? 0.f : ex2(mn - nm[k]);
             l[k] *= f;
-            m[k] = mn;
+            nm[k] = mn;
             if (w == 0 && (lane & 15) == 0) fac[cc] = f;
           }
-          group_sync(1, 128);
+          group_sync(1 + wg, 128);
           if (i > 0) {
             wait_for(pv_done, (t - 1) & 1, bail);
             tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < 4 * NC / 16; ++q) {
+            for (int q = 0; q < 4 * NW / 16; ++q) {
+              const int c0 = c_lo + q * 16 % NW, at = q * 16 / NW * NC + c0;
               uint32_t v[16];
-              tmem_ld16(lanes + q * 16, v);
+              tmem_ld16(lanes + at, v);
               tmem_ld_wait(v);
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                v[k] = __float_as_uint(__uint_as_float(v[k]) * fac[q * 16 % NC + k]);
-              tmem_st16(lanes + q * 16, v);
+                v[k] = __float_as_uint(__uint_as_float(v[k]) * fac[c0 + k]);
+              tmem_st16(lanes + at, v);
             }
             tmem_st_wait();
           }
+#pragma unroll
+          for (int k = 0; k < NH; ++k) y[k] = fmaf(x[k], sl, nm[k]);
         }
-        // p enters the product as bf16 (half a step, 2^-9 of it); its sum is kept in fp32
+        // A column without a reference has seen masked keys (-inf) and NaN only: p of the score
+        // itself. p enters the product as bf16 (half a step, 2^-9 of it); its sum is fp32.
         uint32_t p[NH / 2];
 #pragma unroll
         for (int k = 0; k < NH; k += 2) {
-          const float a0 = ex2(x[k] - (m[k] == -INFINITY ? 0.f : m[k]));
-          const float a1 = ex2(x[k + 1] - (m[k + 1] == -INFINITY ? 0.f : m[k + 1]));
+          const float a0 = ex2(nm[k] == INFINITY ? x[k] : y[k]);
+          const float a1 = ex2(nm[k + 1] == INFINITY ? x[k + 1] : y[k + 1]);
           l[k] += a0;
           l[k + 1] += a1;
           p[k / 2] = pack2(a0, a1);
@@ -518,7 +517,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
           *reinterpret_cast<uint4*>(sm + S::P + sw128_chunk(kk, ch0 / 8 + q, 0)) =
               make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
         if (!F8 && valid < KT) {  // rows past the sequence may hold anything: 0 x NaN is NaN
-          for (int e = tw; e < (KT - valid) * 64; e += 128) {
+          for (int e = tid - 128; e < (KT - valid) * 64; e += 128 * R::kSoft) {
             const int r = valid + (e >> 6), ck = e & 63;
             *reinterpret_cast<uint4*>(sm + S::X + s * kStage + sw128_chunk(r, ck, kAtom)) =
                 make_uint4(0, 0, 0, 0);
@@ -529,7 +528,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
         mbar_arrive(p_full);
       }
       // the segment's sums
-      group_sync(1, 128);  // the last tile's factors are read
+      group_sync(1 + wg, 128);  // the last tile's factors are read
 #pragma unroll
       for (int k = 0; k < NH; ++k) {
         float y = l[k];
@@ -537,30 +536,31 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
         for (int off = 8; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
         if ((lane & 15) == 0) {
           red[w * NC + ch0 + k] = y;
-          if (w == 0) fac[ch0 + k] = m[k];
+          if (w == 0) fac[ch0 + k] = -nm[k];
         }
       }
-      group_sync(1, 128);
+      group_sync(1 + wg, 128);
       const bool whole = wk.st == 0 && wk.cnt == wk.tiles;
       const int slot = wk.st > 0 ? 0 : 1;
       const int64_t part = (c * 2 + slot) * NC;
       const int64_t row0 = static_cast<int64_t>(wk.sn) * a.R + wk.srb * NC;
       const int rows = min(NC, a.R - wk.srb * NC);
+      const int cw = c_lo + tw;  // a thread's column (tw < NW)
       float mul = 1.f;
-      if (tw < NC) {
-        const float ls = (red[tw] + red[NC + tw]) + (red[2 * NC + tw] + red[3 * NC + tw]);
-        const float ms = fac[tw];
+      if (tw < NW) {
+        const float ls = (red[cw] + red[NC + cw]) + (red[2 * NC + cw] + red[3 * NC + cw]);
+        const float ms = fac[cw];
         if (whole) {
           mul = bad ? NAN : ls == 0.f ? 0.f : 1.f / ls;
-          if (tw < rows && d.lse != nullptr)
-            d.lse[row0 + tw] = bad ? NAN : ls == 0.f ? -INFINITY : (ms + log2f(ls)) * kLn2;
+          if (cw < rows && d.lse != nullptr)
+            d.lse[row0 + cw] = bad ? NAN : ls == 0.f ? -INFINITY : (ms + log2f(ls)) * kLn2;
         } else {
-          reinterpret_cast<float2*>(d.ws + wl.ml)[part + tw] = make_float2(ms, bad ? NAN : ls);
+          reinterpret_cast<float2*>(d.ws + wl.ml)[part + cw] = make_float2(ms, bad ? NAN : ls);
         }
       }
-      group_sync(1, 128);
-      if (tw < NC) fac[tw] = mul;
-      if (tw == 0) {
+      group_sync(1 + wg, 128);
+      if (tw < NW) fac[cw] = mul;
+      if (tid == 128) {
         if (bad && d.status != nullptr) atomicExch(d.status, kDevBadPage);
         if (*bail && d.status != nullptr) atomicExch(d.status, kDevWaitTimeout);
         const int64_t u0 = gt - wk.st, u1 = u0 + wk.tiles - 1;  // the unit's first, last tile
@@ -575,15 +575,15 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
           rec->lead = unit;
         }
       }
-      group_sync(1, 128);
+      group_sync(1 + wg, 128);
       wait_for(pv_done, (t - 1) & 1, bail);
       tc_fence_after();
 #pragma unroll 1
-      for (int q = 0; q < 4 * NC / 16; ++q) {
+      for (int q = 0; q < 4 * NW / 16; ++q) {
+        const int c0 = c_lo + q * 16 % NW, mb = q * 16 / NW, ch = mb * 128 + w * 32 + lane;
         uint32_t v[16];
-        tmem_ld16(lanes + q * 16, v);
+        tmem_ld16(lanes + mb * NC + c0, v);
         tmem_ld_wait(v);
-        const int c0 = q * 16 % NC, ch = q * 16 / NC * 128 + w * 32 + lane;
         if (whole) {
           // lane pairs trade values, so that each writes two adjacent channels of a row
 #pragma unroll
@@ -606,85 +606,108 @@ __global__ void __launch_bounds__(F8 ? 512 : 256, 1)
       tc_fence_before();
       mbar_arrive(o_free);
       gt += wk.cnt;
-      group_sync(1, 128);  // fac, red and words are free
+      group_sync(1 + wg, 128);  // fac, red and words are free
     }
   } else if (F8) {
     // ------------------------------------------- 8-bit rows, as bf16 into the stages
-    // Four threads a row; of each 128-channel group one takes the codes 16 q .. and 64 + 16 q ..,
-    // so that 8 threads' stores touch all banks. A group's registers are refilled with the next
-    // tile's codes as soon as they are converted, so ~40 KB an SM are in flight; the block table
-    // is read a tile further ahead.
-    const int i = tid - 256, row = i / 4, qd = i % 4;
-    Walk wl2 = wk;   // runs ahead
-    int li = 0;
-    wl2.cnt = 0;
-    int ahead = 0;
+    reg_dec<R::kRc>();
+    // Sets of eight warps; of two, one takes the even 128-channel groups and one the odd ones
+    // and k_pe. Four threads a row; of a group one takes the codes 16 q .. and 64 + 16 q .., so that
+    // 8 threads' stores touch all banks. A group's registers are refilled with the next tile's
+    // codes as soon as they are converted, so ~40 KB an SM are in flight; the block table is
+    // read a tile further ahead.
+    constexpr int kSets = R::kSets, kMine = 4 / (kSets > 0 ? kSets : 1);  // groups of a set
+    const int i = tid - 128 - 128 * R::kSoft, set = i / 256, row = i % 256 / 4, qd = i % 4;
+    const bool last_set = set == kSets - 1;
+    Walk ahead = wk;
+    int left = n_tiles, in_seg = 0;
+    ahead.cnt = 0;
+    const int shift = 31 - __clz(d.c.page_size);
     struct Row {
-      const unsigned char* p;  // null: no row there
-      bool bad;
+      int page, off;  // page -1: no row there, or (off >= 0) a page out of range
     };
+    // The next tile's place of this thread's row. The page number is not looked at before the
+    // tile after it is being converted, so its load is not waited for.
     auto fetch = [&]() -> Row {
-      if (ahead >= n_tiles) return Row{nullptr, false};
-      ++ahead;
-      if (li == wl2.cnt) {
-        wl2.next(a);
-        li = 0;
+      if (left == 0) return Row{-1, -1};
+      --left;
+      if (in_seg == ahead.cnt) {
+        ahead.next(a);
+        in_seg = 0;
       }
-      const int pos = (wl2.st + li++) * KT + row;
-      if (pos >= wl2.len) return Row{nullptr, false};
-      const int64_t page = d.table[wl2.sn * d.table_pages + pos / d.c.page_size];
-      if (page < 0 || page >= d.c.n_pages) return Row{nullptr, true};
-      return Row{d.c.cache + (page * d.c.page_size + pos % d.c.page_size) * kRow8, false};
+      const int pos = (ahead.st + in_seg++) * KT + row;
+      if (pos >= ahead.len) return Row{-1, -1};
+      return Row{__ldg(d.table + (ahead.sn * d.table_pages + (pos >> shift))),
+                 pos & (d.c.page_size - 1)};
+    };
+    auto place = [&](const Row& r) -> const unsigned char* {
+      if (r.page < 0 || r.page >= d.c.n_pages) return nullptr;
+      return d.c.cache + ((static_cast<int64_t>(r.page) << shift) + r.off) * kRow8;
     };
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    auto ld = [&](const Row& r, int off) {
-      return r.p != nullptr ? __ldg(reinterpret_cast<const uint4*>(r.p + off)) : zero;
+    auto ld = [&](const unsigned char* p, int off) {
+      return p != nullptr ? __ldg(reinterpret_cast<const uint4*>(p + off)) : zero;
     };
-    uint4 code[4][2], pe[2];
+    uint4 code[kMine][2], pe[2];
     uint32_t ex = 0;
-    Row cur = fetch(), nxt = fetch();
+    Row r0 = fetch();
+    const unsigned char* cur = place(r0);
+    bool bad = cur == nullptr && r0.off >= 0;
+    Row nxt = fetch();
+    auto load = [&](const unsigned char* p, int k) {  // group kSets k + set
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+      for (int h = 0; h < 2; ++h) code[k][h] = ld(p, (kSets * k + set) * 128 + h * 64 + qd * 16);
+    };
+    auto load_rest = [&](const unsigned char* p) {
+      if (last_set) {
+        pe[0] = ld(p, kPe8 + qd * 32);
+        pe[1] = ld(p, kPe8 + qd * 32 + 16);
+      }
+      if (p != nullptr) ex = __ldg(reinterpret_cast<const uint32_t*>(p + kExp8));
+    };
 #pragma unroll
-      for (int h = 0; h < 2; ++h) code[g][h] = ld(cur, g * 128 + h * 64 + qd * 16);
-    pe[0] = ld(cur, kPe8 + qd * 32);
-    pe[1] = ld(cur, kPe8 + qd * 32 + 16);
-    ex = cur.p != nullptr ? *reinterpret_cast<const uint32_t*>(cur.p + kExp8) : 0;
+    for (int k = 0; k < kMine; ++k) load(cur, k);
+    load_rest(cur);
+    const uint32_t sw = row & 7;
+    unsigned char* const row_at = sm + S::X + (row >> 3) * 1024 + sw * 128;
     for (int t = 0; t < n_tiles; ++t) {
       const int s = t & 1;
-      const Row nn = fetch();
-      unsigned char* xs = sm + S::X + s * kStage;
-      if (cur.bad) bad_tile[s] = t + 1;
+      const unsigned char* np = place(nxt);
+      const bool nbad = np == nullptr && nxt.off >= 0;
+      nxt = fetch();
+      unsigned char* const dst = row_at + s * kStage;
+      if (bad) bad_tile[s] = t + 1;
+      const uint32_t par = (t / 2 - 1) & 1;
+      auto done = [&](int g) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + s * kGroups + g);
+      };
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int k = 0; k < kMine; ++k) {
+        const int g = kSets * k + set;
         uint32_t v[2][8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          values16(code[g][h], ex >> (8 * g) & 0xffu, v[h]);
-          code[g][h] = ld(nxt, g * 128 + h * 64 + qd * 16);
-        }
-        if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
+        for (int h = 0; h < 2; ++h) values16(code[k][h], ex >> (8 * g) & 0xffu, v[h]);
+        load(np, k);
+        if (t >= 2) wait_for(empty + s * kGroups + g, par, bail);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<uint4*>(xs + sw128_chunk(row, g * 16 + h * 8 + qd * 2 + j, kAtom)) =
+            *reinterpret_cast<uint4*>(dst + (2 * g + h) * kAtom + ((qd * 2 + j) ^ sw) * 16) =
                 make_uint4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full + s * kGroups + g);
+        done(g);
       }
-      if (t >= 2) wait_for(empty + s * kGroups + 4, (t / 2 - 1) & 1, bail);
-      *reinterpret_cast<uint4*>(xs + sw128_chunk(row, 64 + qd * 2, kAtom)) = pe[0];
-      *reinterpret_cast<uint4*>(xs + sw128_chunk(row, 64 + qd * 2 + 1, kAtom)) = pe[1];
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full + s * kGroups + 4);
-      pe[0] = ld(nxt, kPe8 + qd * 32);
-      pe[1] = ld(nxt, kPe8 + qd * 32 + 16);
-      ex = nxt.p != nullptr ? *reinterpret_cast<const uint32_t*>(nxt.p + kExp8) : 0;
-      cur = nxt;
-      nxt = nn;
+      if (last_set) {
+        if (t >= 2) wait_for(empty + s * kGroups + 4, par, bail);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<uint4*>(dst + 8 * kAtom + ((qd * 2 + j) ^ sw) * 16) = pe[j];
+        done(4);
+      }
+      load_rest(np);
+      bad = nbad;
     }
   }
   __syncwarp();
@@ -802,7 +825,7 @@ cudaError_t launch(const DecodeLatentArgs& d, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  kern<<<grid, F8 ? 512 : 256, Sm<NC>::BYTES, st>>>(m, a);
+  kern<<<grid, Roles<NC, F8>::kThreads, Sm<NC>::BYTES, st>>>(m, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
