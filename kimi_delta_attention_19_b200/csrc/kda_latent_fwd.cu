@@ -10,8 +10,10 @@
 // shared k_pe is the third 64-channel column group of every head's keys.
 //
 // The softmax runs a query a thread, on a reference that follows the running maximum lazily:
-// it is raised only when a score passes it by 2^8 (p stays below 256, sums are fp32), and only
-// then is O rescaled.
+// it is raised only when a score passes it by 16 in log2 units (p stays below 2^16; bf16 and
+// the fp32 sums keep their relative precision there), and only then is O rescaled. So the
+// exponentials need not wait for a tile's maximum. P goes over in two halves, the second
+// product starting on the first.
 //
 // Shared memory: the two query tiles (96 KB) and a ring of eight 16 KB column groups
 // [128 keys, 64 channels], five a key tile (k_nope 2, k_pe, v 2).
@@ -24,7 +26,7 @@ namespace {
 constexpr int BM = 128, BN = 128;
 constexpr uint32_t kAtom = BN * 128;     // a column group: 128 rows of 64 bf16
 constexpr int kRing = 8, kPerTile = 5;   // column groups in the ring, of a key tile
-constexpr float kRaise = 8.f;            // log2 units a score may pass its row's reference
+constexpr float kRaise = 16.f;           // log2 units a score may pass its row's reference
 
 struct Sm {
   static constexpr uint32_t Q = 0, RING = 6 * kAtom, BAR = RING + kRing * kAtom, TM = BAR + 256,
@@ -42,7 +44,7 @@ __global__ void __launch_bounds__(384, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Sm::BAR);
   uint64_t *full = bar, *empty = bar + 8, *q_full = bar + 16, *s_full = bar + 18,
-           *p_full = bar + 20, *o_full = bar + 22, *drain = bar + 24, *v_last = bar + 25, *v_fixed = bar + 26;
+           *p_full = bar + 20, *o_full = bar + 22, *drain = bar + 24, *v_last = bar + 25, *v_fixed = bar + 26, *p_half = bar + 27;
   uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + Sm::TM);
   volatile int* bail = reinterpret_cast<volatile int*>(sm + Sm::BAIL);
   const uint32_t sb = smem_u32(sm);
@@ -76,6 +78,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_full + g, 1);
       mbar_init(s_full + g, 1);
+      mbar_init(p_half + g, 128);
       mbar_init(p_full + g, 128);
       mbar_init(o_full + g, 1);
     }
@@ -158,21 +161,23 @@ __global__ void __launch_bounds__(384, 1)
           if (g == 0 || j >= nk[0]) mbar_arrive(v_last);
           wait_for(v_fixed, 0, bail);
         }
-        wait_for(p_full + g, j & 1, bail);
-        tc_fence_after();
         const uint32_t o = tb + 256 + g * 128, p = tb + g * BN;
-        if (c % kRing != kRing - 1) {
-          const uint64_t vb = sdesc_sw128(ring(c), kAtom, 1024);
+        const bool split = c % kRing == kRing - 1;  // the ring's end between v's column groups
+        const uint64_t v0 = sdesc_sw128(ring(c), kAtom, 1024), v1 = sdesc_sw128(ring(c + 1), kAtom, 1024);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_bf16_tmem_a(o, p + 8 * k, vb + 128 * k, iv, j > 0 || k > 0);
-        } else {  // the ring's end between v's two column groups
+        for (int half = 0; half < 2; ++half) {  // of the keys: P arrives in two parts
+          wait_for((half ? p_full : p_half) + g, j & 1, bail);
+          tc_fence_after();
+          if (!split) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint64_t vb = sdesc_sw128(ring(c + i), kAtom, 1024);
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              umma_bf16_tmem_a(o, p + 8 * k, v0 + 128 * k, iv, j > 0 || k > 0);
+          } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_bf16_tmem_a(o + 64 * i, p + 8 * k, vb + 128 * k, ih, j > 0 || k > 0);
+            for (int k = 4 * half; k < 4 * half + 4; ++k) {
+              umma_bf16_tmem_a(o, p + 8 * k, v0 + 128 * k, ih, j > 0 || k > 0);
+              umma_bf16_tmem_a(o + 64, p + 8 * k, v1 + 128 * k, ih, j > 0 || k > 0);
+            }
           }
         }
         if (release) {
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(384, 1)
     const int kend = a.causal ? min(r.lk, max(0, i + 1 + lag)) : r.lk;
     const float sl = a.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
-    float m = -INFINITY;
+    float nm = INFINITY;  // minus the row's reference in log2 units; +inf before its first score
     float2 l2 = make_float2(0.f, 0.f);
     const int nt = nk[g];
     for (int j = 0; j < nt; ++j) {
@@ -233,22 +238,49 @@ __global__ void __launch_bounds__(384, 1)
         for (int k = 0; k < BN; ++k)
           if (k >= lim) v[k / 32][k % 32] = 0xff800000u;
       }
-      float mx[4];
+      // y = log2 of p. The first half's exponentials are taken against the reference as it is
+      // while the second half's maximum is found; both are looked at before P replaces S.
+      float2 nm2 = make_float2(nm, nm);
+      uint32_t p[32];
+      float top = -INFINITY;
+      float2 part = make_float2(0.f, 0.f);
+      auto first_half = [&] {
+        top = -INFINITY;
+        part = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        mx[q] = fmaxf(__uint_as_float(v[q][0]), __uint_as_float(v[q][1]));
+        for (int k = 0; k < 32; ++k) {
+          const float2 y = fma2(make_float2(__uint_as_float(v[k / 16][2 * k % 32]),
+                                            __uint_as_float(v[k / 16][2 * k % 32 + 1])), sl2, nm2);
+          top = fmaxf(top, fmaxf(y.x, y.y));
+          const float2 e = make_float2(ex2(y.x), ex2(y.y));
+          part = add2(part, e);
+          p[k] = pack2(e.x, e.y);
+        }
+      };
+      float mx = -INFINITY;
 #pragma unroll
-        for (int k = 2; k < 32; k += 2)
-          mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(v[q][k]), __uint_as_float(v[q][k + 1])));
-      }
-      const float top = sl * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool up = top > m + kRaise;
-      if (__any_sync(0xffffffffu, up)) {
-        const float mn = up ? top : m, f = m == -INFINITY ? (up ? 0.f : 1.f) : ex2(m - mn);
-        m = mn;
+      for (int k = 0; k < 32; ++k)
+        mx = fmaxf(mx, fmaxf(__uint_as_float(v[2][k]), __uint_as_float(v[3][k])));
+      first_half();
+      const bool up = fmaxf(top, fmaf(mx, sl, nm)) > kRaise;
+      if (__any_sync(0xffffffffu, up || nm == INFINITY)) {
+        // the running maximum becomes the reference of the rows that need it; O and the sum
+        // are rescaled (S of this step comes after O of the last: O is at rest)
+        tmem_ld32(sc, v[0]);
+        tmem_ld32(sc + 32, v[1]);
+        tmem_ld_wait(v[0]);
+        tmem_ld_wait(v[1]);
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          if (k >= lim) v[k / 32][k % 32] = 0xff800000u;
+          mx = fmaxf(mx, __uint_as_float(v[k / 32][k % 32]));
+        }
+        const float n2 = up ? -sl * mx : nm;
+        const float f = nm == INFINITY ? (up ? 0.f : 1.f) : ex2(n2 - nm);
+        nm = n2;
         l2.x *= f;
         l2.y *= f;
-        if (j > 0) {  // S of this step comes after O of the last: O is at rest
+        if (j > 0) {
 #pragma unroll 1
           for (int q = 0; q < 8; ++q) {
             uint32_t o[16];
@@ -259,25 +291,24 @@ __global__ void __launch_bounds__(384, 1)
             tmem_st16(oc + 16 * q, o);
           }
         }
+        const float used = nm == INFINITY ? 0.f : nm;  // no score yet: masked (p = 0) or NaN
+        nm2 = make_float2(used, used);
+        first_half();
       }
-      // p enters the product as bf16 (half a step, 2^-9 of it); its sum is kept in fp32
-      const float nm = m == -INFINITY ? 0.f : -m;
-      const float2 nm2 = make_float2(nm, nm);
+      l2 = add2(l2, part);
+      tmem_st32(sc, p);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(p_half + g);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t p[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int e = 2 * k;
-          float2 x = make_float2(__uint_as_float(v[2 * q + e / 32][e % 32]),
-                                 __uint_as_float(v[2 * q + e / 32][e % 32 + 1]));
-          x = fma2(x, sl2, nm2);
-          x = make_float2(ex2(x.x), ex2(x.y));
-          l2 = add2(l2, x);
-          p[k] = pack2(x.x, x.y);
-        }
-        tmem_st32(sc + 32 * q, p);
+      for (int k = 0; k < 32; ++k) {
+        const float2 y = fma2(make_float2(__uint_as_float(v[2 + k / 16][2 * k % 32]),
+                                          __uint_as_float(v[2 + k / 16][2 * k % 32 + 1])), sl2, nm2);
+        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+        l2 = add2(l2, e);
+        p[k] = pack2(e.x, e.y);
       }
+      tmem_st32(sc + 32, p);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(p_full + g);
@@ -289,7 +320,7 @@ __global__ void __launch_bounds__(384, 1)
     const bool mine = i < r.lq;
     const int64_t row = (r.q0 + i) * a.H + h;
     if (mine && a.lse != nullptr)
-      a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      a.lse[row] = l == 0.f ? -INFINITY : (log2f(l) - nm) * kLn2;
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       uint32_t o[32];
