@@ -10,8 +10,10 @@
 // of CTA are one launch, so that one kind fills the other's tail.
 //
 //   prepare   (lse log2 e, D) a (head, token), one array: the statistics of both kinds
-//   dQ CTA    128 queries, keys 128 at a time: S, dP [q, keys]; dS as bf16 in tensor memory,
-//             the A operand of dQ += dS K
+//   dQ CTA    128 queries, keys 64 at a time: S, dP [q, keys]; dS as bf16 in tensor memory,
+//             the A operand of dQ += dS K. Q and dO are A operands from there too, which
+//             leaves shared memory to the keys: with two stages of 128 keys and Q, dO beside
+//             them the CTA waited for keys half of its time (4300 clocks per 128 keys)
 //   dK CTA    128 keys, queries 64 at a time (what tensor memory leaves): S^T, dP^T [keys, q];
 //             P^T and dS^T the A operands of dV += P^T dO and dK += dS^T Q
 //   k_pe      the heads' fp32 parts of dk_pe, summed in the heads' order
@@ -24,14 +26,15 @@ namespace kda {
 namespace latent {
 namespace {
 
-constexpr int BM = 128;                    // queries of a dQ CTA, keys of a dK CTA, key step of dQ
-constexpr int BQ = 64;                     // query step of a dK CTA
+constexpr int BM = 128;                    // queries of a dQ CTA, keys of a dK CTA
+constexpr int BQ = 64;                     // query step of a dK CTA, key step of a dQ CTA
 constexpr uint32_t kAtom = BM * 128, kAtomQ = BQ * 128;
-constexpr int kQStages = 3;
+constexpr int kQStages = 3, kKStages = 4, kVStages = 3;
 constexpr int kThreads = 384, kSoft = 256;
 
 struct SmQ {  // dQ CTA
-  static constexpr uint32_t Q = 0, DO = 3 * kAtom, K = 5 * kAtom, V = 11 * kAtom, END = 13 * kAtom;
+  static constexpr uint32_t Q = 0, DO = 3 * kAtom, K = 5 * kAtom, V = K + kKStages * 3 * kAtomQ,
+                            END = V + kVStages * 2 * kAtomQ;
 };
 struct SmK {  // dK CTA
   static constexpr uint32_t K = 0, V = 3 * kAtom, ST = 5 * kAtom, STAGE = 5 * kAtomQ,
@@ -42,7 +45,7 @@ constexpr uint32_t kTm = kBar + 256, kBail = kTm + 4, kBytes = kBail + 12;
 static_assert(kBytes <= 232448, "shared memory");
 
 struct Maps {
-  CUtensorMap q, qs, dout, douts, kn, kp, v;  // s: boxes of BQ rows
+  CUtensorMap q, qs, dout, douts, kn, kns, kp, kps, v, vs;  // s: boxes of BQ rows
 };
 
 // (lse log2 e, D) of 32 tokens of a head a block; a row without keys gets +inf: p = 0.
@@ -86,10 +89,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + kBar);
-  uint64_t *full = bar, *empty = bar + 3, *res_full = bar + 6, *s_full = bar + 7, *dp_full = bar + 8,
-           *s_read = bar + 9, *p_ready = bar + 10, *ds_ready = bar + 11, *p_free = bar + 12,
-           *ds_free = bar + 13, *o_full = bar + 14, *v_full = bar + 15, *v_empty = bar + 16,
-           *drain = bar + 17, *last = bar + 18, *fixed = bar + 19;
+  uint64_t *full = bar, *empty = bar + 4, *v_full = bar + 8, *v_empty = bar + 11,
+           *res_full = bar + 14, *s_full = bar + 15, *dp_full = bar + 16, *s_read = bar + 17,
+           *p_ready = bar + 18, *ds_ready = bar + 19, *p_free = bar + 20, *ds_free = bar + 21,
+           *o_full = bar + 22, *drain = bar + 23, *last = bar + 24, *fixed = bar + 25,
+           *a_ready = bar + 26;
   uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + kTm);
   volatile int* bail = reinterpret_cast<volatile int*>(sm + kBail);
   const uint32_t sb = smem_u32(sm);
@@ -114,15 +118,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     j1 = max(j0, (r.lq + BQ - 1) / BQ);
   } else {
     const int last = min(r.lq, b0 + BM);
-    j1 = (min(r.lk, a.causal ? max(0, last + lag) : r.lk) + BM - 1) / BM;
+    j1 = (min(r.lk, a.causal ? max(0, last + lag) : r.lk) + BQ - 1) / BQ;
   }
   const int n = j1 - j0;
 
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
-    }
+    for (int i = 0; i < 14; ++i) mbar_init(bar + i, 1);  // stages, full and empty
     mbar_init(res_full, 1);
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
@@ -132,8 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(p_free, 1);
     mbar_init(ds_free, 1);
     mbar_init(o_full, 1);
-    mbar_init(v_full, 1);
-    mbar_init(v_empty, 1);
+    mbar_init(a_ready, kSoft);
     mbar_init(drain, 1);
     mbar_init(last, 1);
     mbar_init(fixed, 32);
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ======================================================================= dQ
-    constexpr uint32_t S = 0, DP = 128, DS = 256, DQ = 320;  // columns
+    constexpr uint32_t S = 0, DP = 64, DS = 128, QA = 160, GA = 256, DQ = 320;  // columns
     if (warp == 0) {
       if (n > 0 && elect_one()) {
         const int qr = static_cast<int>(r.q0) + b0;
@@ -350,56 +350,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmQ::DO + i * kAtom, &maps.dout, res_full, 64 * i, h, qr);
         int t = 0, tv = 0;
         for (; t < n; ++t) {
-          const int s = t & 1, row = static_cast<int>(r.k0) + t * BM;
-          if (t >= 2) wait_for(empty + s, (t / 2 - 1) & 1, bail);
+          const int s = t % kKStages, sv = t % kVStages, row = static_cast<int>(r.k0) + t * BQ;
+          if (t >= kKStages) wait_for(empty + s, (t / kKStages - 1) & 1, bail);
           if (*bail) break;
-          unsigned char* st = sm + SmQ::K + s * 3 * kAtom;
-          mbar_arrive_expect_tx(full + s, 3 * kAtom);
-          for (int i = 0; i < 2; ++i) tma_load_3d(st + i * kAtom, &maps.kn, full + s, 64 * i, h, row);
-          tma_load_2d(st + 2 * kAtom, &maps.kp, full + s, 0, row);
-          if (t >= 1) wait_for(v_empty, (t - 1) & 1, bail);
+          unsigned char* st = sm + SmQ::K + s * 3 * kAtomQ;
+          mbar_arrive_expect_tx(full + s, 3 * kAtomQ);
+          for (int i = 0; i < 2; ++i) tma_load_3d(st + i * kAtomQ, &maps.kns, full + s, 64 * i, h, row);
+          tma_load_2d(st + 2 * kAtomQ, &maps.kps, full + s, 0, row);
+          if (t >= kVStages) wait_for(v_empty + sv, (t / kVStages - 1) & 1, bail);
           if (*bail) { ++t; break; }
-          mbar_arrive_expect_tx(v_full, 2 * kAtom);
-          for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmQ::V + i * kAtom, &maps.v, v_full, 64 * i, h, row);
+          mbar_arrive_expect_tx(v_full + sv, 2 * kAtomQ);
+          for (int i = 0; i < 2; ++i)
+            tma_load_3d(sm + SmQ::V + (2 * sv + i) * kAtomQ, &maps.vs, v_full + sv, 64 * i, h, row);
           ++tv;
         }
         if (*bail) {  // let the copies in flight land before the CTA ends
           mbar_wait(res_full, 0, 20000000LL);
-          for (int k = t > 2 ? t - 2 : 0; k < t; ++k) mbar_wait(full + (k & 1), k / 2 & 1, 20000000LL);
-          if (tv > 0) mbar_wait(v_full, (tv - 1) & 1, 20000000LL);
+          for (int k = t > kKStages ? t - kKStages : 0; k < t; ++k)
+            mbar_wait(full + k % kKStages, k / kKStages & 1, 20000000LL);
+          for (int k = tv > kVStages ? tv - kVStages : 0; k < tv; ++k)
+            mbar_wait(v_full + k % kVStages, k / kVStages & 1, 20000000LL);
         }
       }
     } else if (warp == 1 && n > 0) {
-      constexpr uint32_t i128 = idesc_bf16(BM, BM, 0, 0), iq = idesc_bf16(BM, 192, 0, 1);
-      const uint64_t q0 = sdesc_sw128(sb + SmQ::Q, 16, 1024), g0 = sdesc_sw128(sb + SmQ::DO, 16, 1024),
-                     v0 = sdesc_sw128(sb + SmQ::V, 16, 1024);
-      auto keys = [&](int t, uint32_t lbo) {
-        return sdesc_sw128(sb + SmQ::K + (t & 1) * 3 * kAtom, lbo, 1024);
-      };
+      constexpr uint32_t i64 = idesc_bf16(BM, BQ, 0, 0), iq = idesc_bf16(BM, 192, 0, 1);
+      auto keys = [&](int t) { return sb + SmQ::K + t % kKStages * 3 * kAtomQ; };
       auto scores = [&](int t) {  // S = Q K^T
-        wait_for(full + (t & 1), t / 2 & 1, bail);
+        wait_for(full + t % kKStages, t / kKStages & 1, bail);
         tc_fence_after();
-        const uint64_t kb = keys(t, 16);
+        const uint64_t kb = sdesc_sw128(keys(t), 16, 1024);
 #pragma unroll
-        for (int k = 0; k < 12; ++k) {
-          const int at = k / 4 * (kAtom / 16) + k % 4 * 2;
-          umma_bf16(tb + S, q0 + at, kb + at, i128, k > 0);
-        }
+        for (int k = 0; k < 12; ++k)
+          umma_bf16_tmem_a(tb + S, tb + QA + 8 * k, kb + k / 4 * (kAtomQ / 16) + k % 4 * 2, i64, k > 0);
         umma_commit(s_full);
       };
       auto dprobs = [&](int t) {  // dP = dO V^T
-        wait_for(v_full, t & 1, bail);
+        const int sv = t % kVStages;
+        wait_for(v_full + sv, t / kVStages & 1, bail);
         tc_fence_after();
+        const uint64_t vb = sdesc_sw128(sb + SmQ::V + 2 * sv * kAtomQ, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int at = k / 4 * (kAtom / 16) + k % 4 * 2;
-          umma_bf16(tb + DP, g0 + at, v0 + at, i128, k > 0);
-        }
+        for (int k = 0; k < 8; ++k)
+          umma_bf16_tmem_a(tb + DP, tb + GA + 8 * k, vb + k / 4 * (kAtomQ / 16) + k % 4 * 2, i64, k > 0);
         umma_commit(dp_full);
-        umma_commit(v_empty);
+        umma_commit(v_empty + sv);
       };
       if (elect_one()) {
-        wait_for(res_full, 0, bail);
+        wait_for(a_ready, 0, bail);
         scores(0);
         dprobs(0);
         for (int t = 0; t < n; ++t) {
@@ -408,16 +405,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_for(ds_ready, t & 1, bail);
           tc_fence_after();
           if (t + 1 < n) dprobs(t + 1);
-          if (r.lk - t * BM < BM) {
+          if (r.lk - t * BQ < BQ) {
             mbar_arrive(last);
             wait_for(fixed, 0, bail);
           }
-          const uint64_t kb = keys(t, kAtom);
+          const uint64_t kb = sdesc_sw128(keys(t), kAtomQ, 1024);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 4; ++k)
             umma_bf16_tmem_a(tb + DQ, tb + DS + 8 * k, kb + 128 * k, iq, t > 0 || k > 0);
           umma_commit(ds_free);
-          umma_commit(empty + (t & 1));
+          umma_commit(empty + t % kKStages);
         }
         umma_commit(o_full);
         if (*bail) {
@@ -425,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(drain, 0, 20000000LL);
         }
       }
-    } else if (warp == 2 && n > 0 && r.lk - (n - 1) * BM < BM) {
+    } else if (warp == 2 && n > 0 && r.lk - (n - 1) * BQ < BQ) {
       // keys past the sequence may hold anything (0 x NaN is NaN): cleared once S is formed
       wait_for(last, 0, bail);
-      zero_rows(sm + SmQ::K + ((n - 1) & 1) * 3 * kAtom, kAtom, 3, r.lk - (n - 1) * BM, BM, lane);
+      zero_rows(sm + SmQ::K + (n - 1) % kKStages * 3 * kAtomQ, kAtomQ, 3, r.lk - (n - 1) * BQ, BQ, lane);
       fence_async_smem();
       mbar_arrive(fixed);
     } else if (warp >= 4) {
@@ -439,47 +436,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 st = mine ? a.stat[h * tq_all + r.q0 + i] : make_float2(INFINITY, 0.f);
       const int kend = a.causal ? min(r.lk, max(0, i + 1 + lag)) : r.lk;
       const float2 nl2 = make_float2(-st.x, -st.x), nd2 = make_float2(-st.y, -st.y);
+      if (n > 0) {  // Q (one warpgroup) and dO (the other) to tensor memory
+        wait_for(res_full, 0, bail);
+        const unsigned char* src = sm + (g ? SmQ::DO : SmQ::Q);
+#pragma unroll 1
+        for (int q = 0; q < (g ? 4 : 6); ++q) {  // 32 channels
+          uint32_t x[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src + sw128_chunk(w * 32 + lane, 4 * q + k, kAtom));
+            x[4 * k] = y.x;
+            x[4 * k + 1] = y.y;
+            x[4 * k + 2] = y.z;
+            x[4 * k + 3] = y.w;
+          }
+          tmem_st16(lanes + (g ? GA : QA) + 16 * q, x);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(a_ready);
+      }
       for (int t = 0; t < n; ++t) {
         wait_for(s_full, t & 1, bail);
         tc_fence_after();
-        uint32_t v[2][32];
-        tmem_ld32(lanes + S + 64 * g, v[0]);
-        tmem_ld32(lanes + S + 64 * g + 32, v[1]);
-        tmem_ld_wait(v[0]);
-        tmem_ld_wait(v[1]);
+        uint32_t v[32];
+        tmem_ld32(lanes + S + 32 * g, v);
+        tmem_ld_wait(v);
         tc_fence_before();
         mbar_arrive(s_read);
-        float2 p[32];
+        float2 p[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float2 x = fma2(make_float2(__uint_as_float(v[k / 16][k % 16 * 2]),
-                                            __uint_as_float(v[k / 16][k % 16 * 2 + 1])), sl2, nl2);
+        for (int k = 0; k < 16; ++k) {
+          const float2 x = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl2, nl2);
           p[k] = make_float2(ex2(x.x), ex2(x.y));
         }
-        const int lim = kend - t * BM - 64 * g;  // keys of this half the query sees
-        const bool cut = __any_sync(0xffffffffu, lim < 64);
+        const int lim = kend - t * BQ - 32 * g;  // keys of this half the query sees
+        const bool cut = __any_sync(0xffffffffu, lim < 32);
         wait_for(dp_full, t & 1, bail);
         tc_fence_after();
-        tmem_ld32(lanes + DP + 64 * g, v[0]);
-        tmem_ld32(lanes + DP + 64 * g + 32, v[1]);
-        tmem_ld_wait(v[0]);
-        tmem_ld_wait(v[1]);
-        uint32_t ds[32];
+        tmem_ld32(lanes + DP + 32 * g, v);
+        tmem_ld_wait(v);
+        uint32_t ds[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float2 x = mul2f(p[k], add2(make_float2(__uint_as_float(v[k / 16][k % 16 * 2]),
-                                                        __uint_as_float(v[k / 16][k % 16 * 2 + 1])), nd2));
+        for (int k = 0; k < 16; ++k) {
+          const float2 x = mul2f(p[k], add2(make_float2(__uint_as_float(v[2 * k]),
+                                                        __uint_as_float(v[2 * k + 1])), nd2));
           ds[k] = pack2(x.x, x.y);
         }
         if (cut) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
+          for (int k = 0; k < 16; ++k) {
             if (2 * k >= lim) ds[k] &= 0xffff0000u;
             if (2 * k + 1 >= lim) ds[k] &= 0x0000ffffu;
           }
         }
         if (t > 0) wait_for(ds_free, (t - 1) & 1, bail);
-        tmem_st32(lanes + DS + 32 * g, ds);
+        tmem_st16(lanes + DS + 16 * g, ds);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(ds_ready);
@@ -553,13 +565,17 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t st) {
       !make_head_map(&m.dout, a.dout, DV, a.H, DV, tq, ot, BM) ||
       !make_head_map(&m.douts, a.dout, DV, a.H, DV, tq, ot, BQ) ||
       !make_head_map(&m.kn, a.kn, DN, a.H, a.kh, tk, a.kt, BM) ||
-      !make_head_map(&m.v, a.v, DV, a.H, a.vh, tk, a.vt, BM))
+      !make_head_map(&m.kns, a.kn, DN, a.H, a.kh, tk, a.kt, BQ) ||
+      !make_head_map(&m.v, a.v, DV, a.H, a.vh, tk, a.vt, BM) ||
+      !make_head_map(&m.vs, a.v, DV, a.H, a.vh, tk, a.vt, BQ))
     return cudaErrorInvalidValue;
   if (tk > 0) {
     const uint64_t dims[2] = {DP, static_cast<uint64_t>(tk)};
     const uint64_t strides[1] = {static_cast<uint64_t>(a.pt) * 2};
-    const uint32_t box[2] = {64, BM};
-    if (!make_tensor_map(&m.kp, a.kp, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    const uint32_t box[2] = {64, BM}, box_s[2] = {64, BQ};
+    if (!make_tensor_map(&m.kp, a.kp, 2, dims, strides, box) ||
+        !make_tensor_map(&m.kps, a.kp, 2, dims, strides, box_s))
+      return cudaErrorInvalidValue;
   }
   cudaError_t e = cudaFuncSetAttribute(bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kBytes);
