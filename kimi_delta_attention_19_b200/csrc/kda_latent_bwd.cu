@@ -48,27 +48,33 @@ struct Maps {
   CUtensorMap q, qs, dout, douts, kn, kns, kp, kps, v, vs;  // s: boxes of BQ rows
 };
 
-// (lse log2 e, D) of 32 tokens of a head a block; a row without keys gets +inf: p = 0.
+// (lse log2 e, D) of 32 tokens of a head a block; a row without keys gets +inf: p = 0. Half a
+// warp a row (16 bytes a lane of dO and of out), all of a warp's loads at once.
 __global__ void __launch_bounds__(256) prepare_kernel(AttnArgs a, int64_t tq) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.y;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 32;
   __shared__ float2 st[32];
+  uint4 x[2], y[2];
+  float l[2];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t t = t0 + warp * 4 + k;
-    if (t >= tq) break;
-    const int64_t row = t * a.H + h;
-    const uint2 x = *reinterpret_cast<const uint2*>(a.dout + row * DV + 4 * lane);
-    const uint2 y = *reinterpret_cast<const uint2*>(a.o + row * DV + 4 * lane);
-    auto lo = [](uint32_t b) { return __uint_as_float(b << 16); };
-    auto hi = [](uint32_t b) { return __uint_as_float(b & 0xffff0000u); };
-    float s = lo(x.x) * lo(y.x) + hi(x.x) * hi(y.x) + lo(x.y) * lo(y.y) + hi(x.y) * hi(y.y);
+  for (int k = 0; k < 2; ++k) {
+    const int64_t t = t0 + warp * 4 + 2 * k + lane / 16, row = (t < tq ? t : tq - 1) * a.H + h;
+    x[k] = *reinterpret_cast<const uint4*>(a.dout + row * DV + 8 * (lane % 16));
+    y[k] = *reinterpret_cast<const uint4*>(a.o + row * DV + 8 * (lane % 16));
+    l[k] = a.lse_in[row];
+  }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (lane == 0) {
-      const float l = a.lse_in[row];
-      st[warp * 4 + k] = make_float2(l == -INFINITY ? INFINITY : l * kLog2e, s);
-    }
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, v[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s += __uint_as_float(u[e] << 16) * __uint_as_float(v[e] << 16) +
+           __uint_as_float(u[e] & 0xffff0000u) * __uint_as_float(v[e] & 0xffff0000u);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (lane % 16 == 0)
+      st[warp * 4 + 2 * k + lane / 16] = make_float2(l[k] == -INFINITY ? INFINITY : l[k] * kLog2e, s);
   }
   __syncthreads();
   if (threadIdx.x < 32 && t0 + threadIdx.x < tq)
@@ -139,6 +145,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(fixed, 32);
     fence_mbar_init();
     *bail = 0;
+    if (n > 0) {  // the CTA's own rows, on their way while it sets up
+      mbar_arrive_expect_tx(res_full, 5 * kAtom);
+      if (is_k) {
+        const int row = static_cast<int>(r.k0) + b0;
+        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmK::K + i * kAtom, &maps.kn, res_full, 64 * i, h, row);
+        tma_load_2d(sm + SmK::K + 2 * kAtom, &maps.kp, res_full, 0, row);
+        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmK::V + i * kAtom, &maps.v, res_full, 64 * i, h, row);
+      } else {
+        const int row = static_cast<int>(r.q0) + b0;
+        for (int i = 0; i < 3; ++i) tma_load_3d(sm + SmQ::Q + i * kAtom, &maps.q, res_full, 64 * i, h, row);
+        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmQ::DO + i * kAtom, &maps.dout, res_full, 64 * i, h, row);
+      }
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem, 512);
@@ -156,11 +175,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t S = 0, DP = 64, P = 128, DS = 160, DVC = 192, DK = 320;  // columns
     if (warp == 0) {
       if (n > 0 && elect_one()) {
-        const int kr = static_cast<int>(r.k0) + b0;
-        mbar_arrive_expect_tx(res_full, 5 * kAtom);
-        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmK::K + i * kAtom, &maps.kn, res_full, 64 * i, h, kr);
-        tma_load_2d(sm + SmK::K + 2 * kAtom, &maps.kp, res_full, 0, kr);
-        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmK::V + i * kAtom, &maps.v, res_full, 64 * i, h, kr);
         int t = 0;
         for (; t < n; ++t) {
           const int s = t % kQStages, row = static_cast<int>(r.q0) + (j0 + t) * BQ;
@@ -305,14 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n > 0) wait_for(o_full, 0, bail);
       tc_fence_after();
-      const bool mine = j < r.lk;
-      const int64_t tok = r.k0 + j, row = tok * a.H + h;
-      // dV: 64 columns a warpgroup; dK: 96 (the second one's last 64 are k_pe's)
+      // dV: 64 columns a warpgroup; dK: 96 (the second one's last 64 are k_pe's, fp32). Through
+      // shared memory, which nothing else needs any more: whole lines go out.
 #pragma unroll 1
       for (int q = 0; q < 10; ++q) {
         uint32_t o[16];
         const bool is_v = q < 4;
-        const int col = is_v ? 64 * g + 16 * q : 96 * g + 16 * (q - 4);
+        const int col = is_v ? 64 * g + 16 * q : 96 * g + 16 * (q - 4), rw = w * 32 + lane;
         if (n > 0) {
           tmem_ld16(lanes + (is_v ? DVC : DK) + col, o);
           tmem_ld_wait(o);
@@ -320,34 +333,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = 0;
         }
-        if (!mine) continue;
         const float mul = is_v ? 1.f : a.scale;
         if (!is_v && col >= DN) {
-          float4* dst = reinterpret_cast<float4*>(a.dpe_part + (h * tk_all + tok) * latent::DP + col - DN);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            dst[k] = make_float4(__uint_as_float(o[4 * k]) * mul, __uint_as_float(o[4 * k + 1]) * mul,
-                                 __uint_as_float(o[4 * k + 2]) * mul, __uint_as_float(o[4 * k + 3]) * mul);
+            *reinterpret_cast<float4*>(sm + SmK::ST + sw128_chunk(rw, (col - DN) / 4 + k, kAtom)) =
+                make_float4(__uint_as_float(o[4 * k]) * mul, __uint_as_float(o[4 * k + 1]) * mul,
+                            __uint_as_float(o[4 * k + 2]) * mul, __uint_as_float(o[4 * k + 3]) * mul);
           continue;
         }
-        uint4* dst = reinterpret_cast<uint4*>((is_v ? a.dv : a.dkn) + row * DN + col);
         uint32_t x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           x[k] = pack2(__uint_as_float(o[2 * k]) * mul, __uint_as_float(o[2 * k + 1]) * mul);
-        dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-        dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        unsigned char* tile = sm + (is_v ? SmK::V : SmK::K);
+        *reinterpret_cast<uint4*>(tile + sw128_chunk(rw, col / 8, kAtom)) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(tile + sw128_chunk(rw, col / 8 + 1, kAtom)) = make_uint4(x[4], x[5], x[6], x[7]);
       }
+      group_sync(3, kSoft);
+      const int rows = min(BM, r.lk - b0);
+      const int64_t tok = r.k0 + b0, at = (tok * a.H + h) * DN, step = static_cast<int64_t>(a.H) * DN * 2;
+      copy_rows<2>(sm + SmK::V, reinterpret_cast<unsigned char*>(a.dv + at), step, 0, rows, warp - 4, 8, lane);
+      copy_rows<2>(sm + SmK::K, reinterpret_cast<unsigned char*>(a.dkn + at), step, 0, rows, warp - 4, 8, lane);
+      copy_rows<2>(sm + SmK::ST, reinterpret_cast<unsigned char*>(a.dpe_part + (h * tk_all + tok) * latent::DP),
+                   latent::DP * 4, 0, rows, warp - 4, 8, lane);
     }
   } else {
     // ======================================================================= dQ
     constexpr uint32_t S = 0, DP = 64, DS = 128, QA = 160, GA = 256, DQ = 320;  // columns
     if (warp == 0) {
       if (n > 0 && elect_one()) {
-        const int qr = static_cast<int>(r.q0) + b0;
-        mbar_arrive_expect_tx(res_full, 5 * kAtom);
-        for (int i = 0; i < 3; ++i) tma_load_3d(sm + SmQ::Q + i * kAtom, &maps.q, res_full, 64 * i, h, qr);
-        for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmQ::DO + i * kAtom, &maps.dout, res_full, 64 * i, h, qr);
         int t = 0, tv = 0;
         for (; t < n; ++t) {
           const int s = t % kKStages, sv = t % kVStages, row = static_cast<int>(r.k0) + t * BQ;
@@ -498,9 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n > 0) wait_for(o_full, 0, bail);
       tc_fence_after();
-      const int64_t row = (r.q0 + i) * a.H + h;
 #pragma unroll 1
-      for (int q = 0; q < 6; ++q) {
+      for (int q = 0; q < 6; ++q) {  // through shared memory: whole lines go out
         uint32_t o[16];
         if (n > 0) {
           tmem_ld16(lanes + DQ + 96 * g + 16 * q, o);
@@ -509,15 +523,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = 0;
         }
-        if (!mine) continue;
-        uint4* dst = reinterpret_cast<uint4*>(a.dq + row * DQK + 96 * g + 16 * q);
         uint32_t x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           x[k] = pack2(__uint_as_float(o[2 * k]) * a.scale, __uint_as_float(o[2 * k + 1]) * a.scale);
-        dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-        dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<uint4*>(sm + SmQ::Q + sw128_chunk(w * 32 + lane, 12 * g + 2 * q + k, kAtom)) =
+              make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
       }
+      group_sync(3, kSoft);
+      copy_rows<3>(sm + SmQ::Q, reinterpret_cast<unsigned char*>(a.dq + ((r.q0 + b0) * a.H + h) * DQK),
+                   static_cast<int64_t>(a.H) * DQK * 2, 0, min(BM, r.lq - b0), warp - 4, 8, lane);
     }
   }
   __syncwarp();

@@ -87,6 +87,13 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(v_fixed, 32);
     fence_mbar_init();
     *bail = 0;
+    for (int g = 0; g < 2; ++g) {  // on their way while the CTA sets up
+      if (nk[g] == 0) continue;
+      mbar_arrive_expect_tx(q_full + g, 3 * kAtom);
+      for (int i = 0; i < 3; ++i)
+        tma_load_3d(sm + Sm::Q + (3 * g + i) * kAtom, &maps.q, q_full + g, 64 * i, h,
+                    static_cast<int>(r.q0) + i0 + g * BM);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem, 512);
@@ -102,13 +109,6 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 0) {
       // ---------------------------------------------------------------- loads
       if (elect_one()) {
-        for (int g = 0; g < 2; ++g) {
-          if (nk[g] == 0) continue;
-          mbar_arrive_expect_tx(q_full + g, 3 * kAtom);
-          for (int i = 0; i < 3; ++i)
-            tma_load_3d(sm + Sm::Q + (3 * g + i) * kAtom, &maps.q, q_full + g, 64 * i, h,
-                        static_cast<int>(r.q0) + i0 + g * BM);
-        }
         int c = 0;
         for (int j = 0; j < n; ++j) {
           const int row = static_cast<int>(r.k0) + j * BN;
@@ -321,6 +321,8 @@ __global__ void __launch_bounds__(384, 1)
     const int64_t row = (r.q0 + i) * a.H + h;
     if (mine && a.lse != nullptr)
       a.lse[row] = l == 0.f ? -INFINITY : (log2f(l) - nm) * kLn2;
+    // through shared memory (the tile's queries are not needed any more): whole lines go out
+    unsigned char* tile = sm + Sm::Q + 3 * g * kAtom;
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       uint32_t o[32];
@@ -331,19 +333,21 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = 0;
       }
-      if (mine) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + row * DV + 32 * q);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t x[4];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = pack2(__uint_as_float(o[8 * k + 2 * e]) * mul,
-                         __uint_as_float(o[8 * k + 2 * e + 1]) * mul);
-          dst[k] = make_uint4(x[0], x[1], x[2], x[3]);
-        }
+        for (int e = 0; e < 4; ++e)
+          x[e] = pack2(__uint_as_float(o[8 * k + 2 * e]) * mul,
+                       __uint_as_float(o[8 * k + 2 * e + 1]) * mul);
+        *reinterpret_cast<uint4*>(tile + sw128_chunk(w * 32 + lane, 4 * q + k, kAtom)) =
+            make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
+    __syncwarp();
+    const int first = i0 + g * BM + w * 32;  // this warp's rows
+    copy_rows<2>(tile, reinterpret_cast<unsigned char*>(a.out + ((r.q0 + first) * a.H + h) * DV),
+                 static_cast<int64_t>(a.H) * DV * 2, w * 32, min(32, r.lq - first), 0, 1, lane);
     if (tid == 128 && *bail && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
   }
   __syncwarp();

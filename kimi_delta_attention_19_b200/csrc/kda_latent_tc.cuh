@@ -117,6 +117,20 @@ __device__ __forceinline__ void reg_inc() {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Rows of a staged tile ([128 rows, 128 bytes] swizzled column groups, kRowAtom bytes each) to
+// global memory, whole 128-byte lines a quarter warp; `rows` are copied, by `warps` warps.
+constexpr uint32_t kRowAtom = 128 * 128;
+template <int kGroupsOut>
+__device__ __forceinline__ void copy_rows(const unsigned char* tile, unsigned char* dst,
+                                          int64_t row_bytes, int row0, int rows, int warp,
+                                          int warps, int lane) {
+  for (int e = warp * 4 + lane / 8; e < rows * kGroupsOut; e += warps * 4) {
+    const int row = row0 + e / kGroupsOut, at = e % kGroupsOut, c = lane % 8;
+    *reinterpret_cast<uint4*>(dst + (e / kGroupsOut) * row_bytes + at * 128 + c * 16) =
+        *reinterpret_cast<const uint4*>(tile + sw128_chunk(row, at * 8 + c, kRowAtom));
+  }
+}
+
 // Tiled bf16 tensor map of `rank` dimensions (the innermost one contiguous, strides in bytes
 // of the others), whose boxes land in the 128-byte-swizzled operand layout.
 bool make_tensor_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
