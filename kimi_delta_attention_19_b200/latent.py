@@ -15,6 +15,7 @@ device and on `stream` (default: that device's current stream).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -76,44 +77,47 @@ EXPORTED = ("kda_latent_attn_fwd", "kda_latent_attn_bwd_workspace_size", "kda_la
 # The checks of a call are plain conditions (messages are formed only when one fails), pointers
 # and streams go to the library as integers and structs are filled by position: a call that
 # launches one small kernel costs the host more than the GPU otherwise.
-def _typed(t: torch.Tensor | None, dtype: torch.dtype, shape, name: str, device) -> int | None:
-    """Checks an optional contiguous tensor argument on `device`; its address."""
+def _typed(t: torch.Tensor | None, dtype: torch.dtype, shape, name: str, index: int) -> int | None:
+    """Checks an optional contiguous tensor argument on GPU `index`; its address."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are not")
     return t.data_ptr()
 
 
-def _bf16(t: torch.Tensor, name: str, device) -> None:
-    if t.dtype != torch.bfloat16:
+def _bf16(t: torch.Tensor, name: str, index: int) -> None:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"unsupported dtype {t.dtype} of {name}: latent attention takes bfloat16")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are not")
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
     else lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
-def _launch(device: torch.device, stream, call):
-    """`call(raw stream)` with the tensors' device and the call's stream current (so that
-    what it allocates belongs to them). Without a GPU tensor it refuses."""
-    if device.type != "cuda":
-        raise ValueError(f"latent attention needs CUDA tensors (got {device})")
-    if stream is not None:
-        with torch.cuda.device(device), torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return call(_raw_stream(device.index))
-    return call(_raw_stream(device.index))
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call on GPU `index` and `stream` has to make them current first."""
+    if index < 0:
+        raise ValueError("latent attention needs CUDA tensors")
+    return stream is not None or torch.cuda.current_device() != index
+
+
+@contextlib.contextmanager
+def _there(index: int, stream):
+    with torch.cuda.device(index):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
 
 
 def _addr(t: torch.Tensor | None) -> int | None:
@@ -128,8 +132,10 @@ def _check(rc: int, what: str) -> None:
 # ------------------------------------------------------------------------ expanded form
 def _strides(t: torch.Tensor, name: str, batched: bool):
     """(token, head) strides of [.., T, H, d], or (token, 0) of k_pe [.., T, d], in elements."""
-    head = name != "k_pe"
     st, shape = t.stride(), t.shape
+    if len(shape) == 3 and shape[0] > 1 and shape[1] > 1 and st[2] == 1 and name != "k_pe":
+        return st[0], st[1]
+    head = name != "k_pe"
     if st[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}'s channels must be contiguous")
     token = st[-3] if head else st[-2]
@@ -142,19 +148,20 @@ def _strides(t: torch.Tensor, name: str, batched: bool):
     return token, hs
 
 
-def _attn_shape(q, k_nope, k_pe, v, cu_q, cu_k, max_q, max_k, causal, scale):
-    dev, qs, ks, vs, ps = q.device, q.shape, k_nope.shape, v.shape, k_pe.shape
-    _bf16(q, "q", dev)
-    _bf16(k_nope, "k_nope", dev)
-    _bf16(k_pe, "k_pe", dev)
-    _bf16(v, "v", dev)
+def _attn_shape(q, k_nope, k_pe, v, cu_q, cu_k, max_q, max_k, causal, scale, index):
+    qs, ks, vs, ps = q.shape, k_nope.shape, v.shape, k_pe.shape
+    _bf16(q, "q", index)
+    _bf16(k_nope, "k_nope", index)
+    _bf16(k_pe, "k_pe", index)
+    _bf16(v, "v", index)
     dim = len(qs)
     batched = dim == 4
     if dim not in (3, 4) or len(ks) != dim or len(vs) != dim or len(ps) != dim - 1:
         raise ValueError("q, k_nope, v must be [T, H, d] or [B, T, H, d] and k_pe [T, d] or "
                          "[B, T, d]")
-    H = qs[-2]
-    if ks[-2] != H or vs[:-1] != ks[:-1] or ps[:-1] != ks[:-2] or (batched and qs[0] != ks[0]):
+    H, Tk = qs[-2], ks[-3]
+    if ks[-2] != H or vs[-2] != H or vs[-3] != Tk or ps[-2] != Tk or \
+            (batched and not qs[0] == ks[0] == vs[0] == ps[0]):
         raise ValueError(f"shapes do not agree: q {tuple(qs)}, k_nope {tuple(ks)}, "
                          f"k_pe {tuple(ps)}, v {tuple(vs)}")
     if qs[-1] != ks[-1] + ps[-1]:
@@ -165,17 +172,17 @@ def _attn_shape(q, k_nope, k_pe, v, cu_q, cu_k, max_q, max_k, causal, scale):
     if cu_q is not None:
         if cu_q.dim() != 1 or cu_q.numel() < 2:
             raise ValueError("cu_seqlens must hold n_seqs + 1 offsets")
-        _typed(cu_q, torch.int32, None, "cu_seqlens", dev)
+        _typed(cu_q, torch.int32, None, "cu_seqlens", index)
         if cu_k is not cu_q:
-            _typed(cu_k, torch.int32, cu_q.shape, "cu_seqlens_k", dev)
+            _typed(cu_k, torch.int32, cu_q.shape, "cu_seqlens_k", index)
         n_seqs = cu_q.numel() - 1
     qt, qh = _strides(q, "q", batched)
     kt, kh = _strides(k_nope, "k_nope", batched)
     vt, vh = _strides(v, "v", batched)
     pt, _ = _strides(k_pe, "k_pe", batched)
-    return LatentShape(qs[0] if batched else 1, H, qs[-3], ks[-3], n_seqs, int(max_q),
-                       int(max_k), ks[-1], ps[-1], vs[-1], qt, qh, kt, kh, pt, vt, vh,
-                       int(bool(causal)), KDA_BF16, 0.0 if scale is None else float(scale))
+    return LatentShape(qs[0] if batched else 1, H, qs[-3], Tk, n_seqs, int(max_q), int(max_k),
+                       ks[-1], ps[-1], vs[-1], qt, qh, kt, kh, pt, vt, vh, int(bool(causal)),
+                       KDA_BF16, 0.0 if scale is None else float(scale))
 
 
 def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
@@ -197,24 +204,28 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v
     """
     if cu_seqlens is not None and cu_seqlens_k is None:
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
+    at = q.get_device()
+    if _elsewhere(at, stream):
+        with _there(at, stream):
+            return latent_attn_fwd(q, k_nope, k_pe, v, cu_seqlens=cu_seqlens,
+                                   cu_seqlens_k=cu_seqlens_k, max_seqlen=max_seqlen,
+                                   max_seqlen_k=max_seqlen_k, causal=causal, scale=scale, out=out,
+                                   lse=lse, status=status)
     s = _attn_shape(q, k_nope, k_pe, v, cu_seqlens, cu_seqlens_k, max_seqlen, max_seqlen_k,
-                    causal, scale)
-    dev, lead = q.device, q.shape[:-1]
-    _typed(out, torch.bfloat16, lead + v.shape[-1:], "out", dev)
-    _typed(lse, torch.float32, lead, "lse", dev)
-    status_p = _typed(status, torch.int32, None, "status", dev)
-
-    def call(st):
-        nonlocal out, lse
-        if out is None:
-            out = torch.empty(lead + v.shape[-1:], dtype=q.dtype, device=dev)
-        if lse is None:
-            lse = torch.empty(lead, dtype=torch.float32, device=dev)
-        return lib.kda_latent_attn_fwd(
-            q.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), v.data_ptr(), _addr(cu_seqlens),
-            _addr(cu_seqlens_k), out.data_ptr(), lse.data_ptr(), ctypes.byref(s), status_p, st)
-
-    _check(_launch(dev, stream, call), "kda_latent_attn_fwd")
+                    causal, scale, at)
+    lead = q.shape[:-1]
+    if out is None:
+        out = q.new_empty(lead + v.shape[-1:])
+    else:
+        _typed(out, torch.bfloat16, lead + v.shape[-1:], "out", at)
+    if lse is None:
+        lse = q.new_empty(lead, dtype=torch.float32)
+    else:
+        _typed(lse, torch.float32, lead, "lse", at)
+    _check(lib.kda_latent_attn_fwd(
+        q.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), v.data_ptr(), _addr(cu_seqlens),
+        _addr(cu_seqlens_k), out.data_ptr(), lse.data_ptr(), ctypes.byref(s),
+        _typed(status, torch.int32, None, "status", at), _raw_stream(at)), "kda_latent_attn_fwd")
     return out, lse
 
 
@@ -232,36 +243,40 @@ def latent_attn_bwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v
     and latent_attn_fwd."""
     if cu_seqlens is not None and cu_seqlens_k is None:
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
+    at = q.get_device()
+    if _elsewhere(at, stream):
+        with _there(at, stream):
+            return latent_attn_bwd(q, k_nope, k_pe, v, out, lse, d_out, cu_seqlens=cu_seqlens,
+                                   cu_seqlens_k=cu_seqlens_k, max_seqlen=max_seqlen,
+                                   max_seqlen_k=max_seqlen_k, causal=causal, scale=scale,
+                                   grads=grads, workspace=workspace, status=status)
     s = _attn_shape(q, k_nope, k_pe, v, cu_seqlens, cu_seqlens_k, max_seqlen, max_seqlen_k,
-                    causal, scale)
-    dev, lead = q.device, q.shape[:-1]
-    out_p = _typed(out, torch.bfloat16, lead + v.shape[-1:], "out", dev)
-    lse_p = _typed(lse, torch.float32, lead, "lse", dev)
-    d_out_p = _typed(d_out, torch.bfloat16, lead + v.shape[-1:], "d_out", dev)
-    status_p = _typed(status, torch.int32, None, "status", dev)
-    _typed(workspace, torch.uint8, None, "workspace", dev)
+                    causal, scale, at)
+    lead = q.shape[:-1]
+    out_p = _typed(out, torch.bfloat16, lead + v.shape[-1:], "out", at)
+    lse_p = _typed(lse, torch.float32, lead, "lse", at)
+    d_out_p = _typed(d_out, torch.bfloat16, lead + v.shape[-1:], "d_out", at)
+    status_p = _typed(status, torch.int32, None, "status", at)
     like = (q, k_nope, k_pe, v)
-    if grads is not None:
+    if grads is None:
+        grads = tuple(q.new_empty(t.shape) for t in like)
+    else:
         if len(grads) != 4:
             raise ValueError("grads must be (dq, dk_nope, dk_pe, dv)")
         for g, t, name in zip(grads, like, ("dq", "dk_nope", "dk_pe", "dv")):
-            _typed(g, torch.bfloat16, t.shape, name, dev)
-
-    def call(st):
-        nonlocal grads, workspace
-        if grads is None:
-            grads = tuple(torch.empty(t.shape, dtype=t.dtype, device=dev) for t in like)
-        if workspace is None:
-            nbytes = lib.kda_latent_attn_bwd_workspace_size(ctypes.byref(s))
-            if nbytes == 0:
-                raise KdaError(KDA_ERR_INVALID_ARG, "kda_latent_attn_bwd_workspace_size")
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        return lib.kda_latent_attn_bwd(
-            q.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), v.data_ptr(), out_p, lse_p,
-            d_out_p, _addr(cu_seqlens), _addr(cu_seqlens_k), *(g.data_ptr() for g in grads),
-            ctypes.byref(s), workspace.data_ptr(), workspace.numel(), status_p, st)
-
-    _check(_launch(dev, stream, call), "kda_latent_attn_bwd")
+            _typed(g, torch.bfloat16, t.shape, name, at)
+    if workspace is None:
+        nbytes = lib.kda_latent_attn_bwd_workspace_size(ctypes.byref(s))
+        if nbytes == 0:
+            raise KdaError(KDA_ERR_INVALID_ARG, "kda_latent_attn_bwd_workspace_size")
+        workspace = q.new_empty(nbytes, dtype=torch.uint8)
+    else:
+        _typed(workspace, torch.uint8, None, "workspace", at)
+    _check(lib.kda_latent_attn_bwd(
+        q.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), v.data_ptr(), out_p, lse_p, d_out_p,
+        _addr(cu_seqlens), _addr(cu_seqlens_k), *(g.data_ptr() for g in grads), ctypes.byref(s),
+        workspace.data_ptr(), workspace.numel(), status_p, _raw_stream(at)),
+        "kda_latent_attn_bwd")
     return tuple(grads)
 
 
@@ -338,20 +353,22 @@ def latent_cache_write(latent: torch.Tensor, k_pe: torch.Tensor, cache: torch.Te
     strided) to rows slots [T] (int64: page * page_size + offset). Negative slots are
     skipped (padding); one past the cache is skipped and reported as 3 in `status` (int32
     device tensor). Slots must be distinct."""
-    cs, dev, T = _cache_shape(cache), cache.device, latent.shape[0]
+    at = cache.get_device()
+    if _elsewhere(at, stream):
+        with _there(at, stream):
+            return latent_cache_write(latent, k_pe, cache, slots, status=status)
+    cs, T = _cache_shape(cache), latent.shape[0]
     for t, name, d in ((latent, "latent", D_C), (k_pe, "k_pe", D_PE)):
-        _bf16(t, name, dev)
+        _bf16(t, name, at)
         if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1:
             raise ValueError(f"{name} must be [T, {d}] with contiguous channels")
     if k_pe.shape[0] != T:
         raise ValueError("latent and k_pe must have the same tokens")
-    slots_p = _typed(slots, torch.int64, latent.shape[:1], "slots", dev)
-    status_p = _typed(status, torch.int32, None, "status", dev)
-    args = (latent.data_ptr(), latent.stride(0) if T > 1 else D_C, k_pe.data_ptr(),
-            k_pe.stride(0) if T > 1 else D_PE, slots_p, T, cache.data_ptr(), ctypes.byref(cs),
-            status_p)
-    _check(_launch(dev, stream, lambda st: lib.kda_latent_cache_write(*args, st)),
-           "kda_latent_cache_write")
+    _check(lib.kda_latent_cache_write(
+        latent.data_ptr(), latent.stride(0) if T > 1 else D_C, k_pe.data_ptr(),
+        k_pe.stride(0) if T > 1 else D_PE, _typed(slots, torch.int64, (T,), "slots", at), T,
+        cache.data_ptr(), ctypes.byref(cs), _typed(status, torch.int32, None, "status", at),
+        _raw_stream(at)), "kda_latent_cache_write")
 
 
 def latent_cache_read(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -363,31 +380,31 @@ def latent_cache_read(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens
     then k_pe), for instance to expand a cached prefix in front of new queries. block_table
     is int32 [n, pages]. A token past its table or with a page out of range is NaN and
     reported as 3 in `status`; rows behind the last sequence are not written."""
-    cs, dev = _cache_shape(cache), cache.device
-    cu_p = _typed(cu_seqlens, torch.int32, None, "cu_seqlens", dev)
+    at = cache.get_device()
+    if _elsewhere(at, stream):
+        with _there(at, stream):
+            return latent_cache_read(cache, block_table, cu_seqlens, total=total, starts=starts,
+                                     out=out, status=status)
+    cs = _cache_shape(cache)
+    cu_p = _typed(cu_seqlens, torch.int32, None, "cu_seqlens", at)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must hold n_seqs + 1 offsets")
     n = cu_seqlens.numel() - 1
-    table_p = _typed(block_table, torch.int32, None, "block_table", dev)
+    table_p = _typed(block_table, torch.int32, None, "block_table", at)
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError(f"block_table must be [{n}, pages] (got {tuple(block_table.shape)})")
-    starts_p = _typed(starts, torch.int32, (n,), "starts", dev)
-    status_p = _typed(status, torch.int32, None, "status", dev)
     if out is not None:
         _typed(out, torch.bfloat16, (out.shape[0] if total is None else total, D_C + D_PE),
-               "out", dev)
+               "out", at)
     elif total is None:
         raise ValueError("total (rows of the result) or out is needed")
-
-    def call(st):
-        nonlocal out
-        if out is None:
-            out = torch.empty(total, D_C + D_PE, dtype=torch.bfloat16, device=dev)
-        return lib.kda_latent_cache_read(cache.data_ptr(), table_p, block_table.shape[1], cu_p,
-                                         starts_p, n, out.shape[0], out.data_ptr(),
-                                         ctypes.byref(cs), status_p, st)
-
-    _check(_launch(dev, stream, call), "kda_latent_cache_read")
+    else:
+        out = cache.new_empty((total, D_C + D_PE), dtype=torch.bfloat16)
+    _check(lib.kda_latent_cache_read(
+        cache.data_ptr(), table_p, block_table.shape[1], cu_p,
+        _typed(starts, torch.int32, (n,), "starts", at), n, out.shape[0], out.data_ptr(),
+        ctypes.byref(cs), _typed(status, torch.int32, None, "status", at), _raw_stream(at)),
+        "kda_latent_cache_read")
     return out
 
 
@@ -411,52 +428,54 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     out = 0, lse = -inf. seq_lens past the table or a page out of range: NaN rows and 3 in
     `status`. `workspace` may be kept (latent_decode_workspace); it serves one call at a time.
     """
-    cs, dev, qs = _cache_shape(cache), cache.device, q.shape
-    _bf16(q, "q", dev)
+    at = cache.get_device()
+    if _elsewhere(at, stream):
+        with _there(at, stream):
+            return latent_decode(q, cache, block_table, seq_lens, draft_mask=draft_mask,
+                                 scale=scale, out=out, lse=lse, workspace=workspace,
+                                 status=status)
+    cs, qs = _cache_shape(cache), q.shape
+    _bf16(q, "q", at)
     dim = len(qs)
     if dim not in (3, 4) or qs[-1] != D_C + D_PE:
         raise ValueError(f"q must be [N, H, {D_C + D_PE}] or [N, L, H, {D_C + D_PE}] "
                          f"(got {tuple(qs)})")
     N, L, H = qs[0], qs[1] if dim == 4 else 1, qs[-2]
     lead = qs[:-1]
-    q_p = _typed(q, torch.bfloat16, None, "q", dev)
-    table_p = _typed(block_table, torch.int32, None, "block_table", dev)
+    q_p = _typed(q, torch.bfloat16, None, "q", at)
+    table_p = _typed(block_table, torch.int32, None, "block_table", at)
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError(f"block_table must be [{N}, pages] (got {tuple(block_table.shape)})")
-    lens_p = _typed(seq_lens, torch.int32, (N,), "seq_lens", dev)
-    mask_p = _typed(draft_mask, torch.int64, (N, L), "draft_mask", dev)
-    _typed(out, torch.bfloat16, lead + (D_C,), "out", dev)
-    lse_p = _typed(lse, torch.float32, lead, "lse", dev)
-    _typed(workspace, torch.uint8, None, "workspace", dev)
-    status_p = _typed(status, torch.int32, None, "status", dev)
     s = DecodeShape(N, L, H, block_table.shape[1], KDA_BF16, 0.0 if scale is None else float(scale))
-
-    def call(st):
-        nonlocal out, workspace
-        if out is None:
-            out = torch.empty(lead + (D_C,), dtype=torch.bfloat16, device=dev)
-        if workspace is None:
-            workspace = _decode_workspace(s, cs, dev)
-        return lib.kda_latent_decode(q_p, cache.data_ptr(), table_p, lens_p, mask_p,
-                                     out.data_ptr(), lse_p, ctypes.byref(s), ctypes.byref(cs),
-                                     workspace.data_ptr(), workspace.numel(), status_p, st)
-
-    _check(_launch(dev, stream, call), "kda_latent_decode")
+    if out is None:
+        out = q.new_empty(lead + (D_C,))
+    else:
+        _typed(out, torch.bfloat16, lead + (D_C,), "out", at)
+    if workspace is None:
+        workspace = _decode_workspace(s, cs, cache)
+    else:
+        _typed(workspace, torch.uint8, None, "workspace", at)
+    _check(lib.kda_latent_decode(
+        q_p, cache.data_ptr(), table_p, _typed(seq_lens, torch.int32, (N,), "seq_lens", at),
+        _typed(draft_mask, torch.int64, (N, L), "draft_mask", at), out.data_ptr(),
+        _typed(lse, torch.float32, lead, "lse", at), ctypes.byref(s), ctypes.byref(cs),
+        workspace.data_ptr(), workspace.numel(), _typed(status, torch.int32, None, "status", at),
+        _raw_stream(at)), "kda_latent_decode")
     return out
 
 
-def _decode_workspace(s: DecodeShape, cs: CacheShape, device) -> torch.Tensor:
-    n = int(lib.kda_latent_decode_workspace_size(ctypes.byref(s), ctypes.byref(cs)))
+def _decode_workspace(s: DecodeShape, cs: CacheShape, cache: torch.Tensor) -> torch.Tensor:
+    n = lib.kda_latent_decode_workspace_size(ctypes.byref(s), ctypes.byref(cs))
     if n == 0:
         raise KdaError(KDA_ERR_INVALID_ARG, "kda_latent_decode_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return cache.new_empty(n, dtype=torch.uint8)
 
 
 def latent_decode_workspace(N: int, H: int, cache: torch.Tensor, *, L: int = 1) -> torch.Tensor:
     """Scratch for latent_decode calls of N sequences, L query tokens and H heads."""
     with torch.cuda.device(cache.device):
         return _decode_workspace(DecodeShape(N=N, L=L, H=H, dtype=KDA_BF16),
-                                 _cache_shape(cache), cache.device)
+                                 _cache_shape(cache), cache)
 
 
 status_of = kda.workspace_status   # (status, device code) of a status word
