@@ -720,79 +720,117 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
 }
 
 // Joins the partials of the units that runs cut: sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
-// over the CTAs of a unit, in their order. Four rows a block (128 threads each, 4 channels a
-// thread); a unit of more than 8 CTAs gives every row a block of its own (the blocks of the
-// CTAs in between help), whose four groups each take a quarter of the partials.
+// over the CTAs of a unit, in their order. Usually those are two: sixteen rows a block, the
+// partials of its CTA and the next fetched before it is known whether they belong together (the
+// kernel is a chain of memory latencies). Another unit is shared by the blocks of all of
+// them: a (row, quarter of the channels) is a warp's work, or a block's from 65 CTAs on, its
+// partials spread over the block's 16 warps and summed in the warps' order.
+constexpr int kJoinRows = 16;
+
+__device__ __forceinline__ void put_row(const Args& a, int64_t row, int ch, float4 acc, float M, float l) {
+  const bool nan = l != l;  // poisons rows whose partials were not
+  const float mul = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>(a.d.out + row * DC + ch) =
+      nan ? make_uint2(0x7fff7fffu, 0x7fff7fffu)
+          : make_uint2(pack2(acc.x * mul, acc.y * mul), pack2(acc.z * mul, acc.w * mul));
+  if (ch == 0 && a.d.lse != nullptr)
+    a.d.lse[row] = nan ? l : l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
+// a partial's weight against the joint reference, and what it adds to the sum
+__device__ __forceinline__ float weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
+__device__ __forceinline__ float share(float f, float l) { return l != l ? l : f * l; }  // NaN: a bad page
+
 template <int NC>
 __global__ void __launch_bounds__(512) join_kernel(const Args a) {
-  griddep_wait();
-  const Rec r = reinterpret_cast<const Rec*>(a.d.ws)[blockIdx.x];
   const Layout wl = ws_layout(NC);
   const float2* ml = reinterpret_cast<const float2*>(a.d.ws + wl.ml);
   const float* part = reinterpret_cast<const float*>(a.d.ws + wl.part);
-  __shared__ float4 acc_s[4][128];
-  __shared__ float ml_s[4][2];
-  const int grp = threadIdx.x / 128, th = threadIdx.x % 128;
+  __shared__ float4 acc_s[16][32];
+  __shared__ float2 ml_s[16];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  griddep_wait();
+  constexpr bool kPairs = NC <= 32;  // (of 64 rows the unneeded loads cost more: 111 us for 104)
+  constexpr int kRows = kJoinRows / 4;  // of a thread
+  float2 x[kRows][2];
+  float4 o[kRows][2];
+#pragma unroll
+  for (int k = 0; kPairs && k < kRows; ++k)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int c = min(static_cast<int>(blockIdx.x) + p, kMaxCtas - 1);
+      const int i = (c * 2 + 1 - p) * NC + blockIdx.y * kJoinRows + k * 4 + threadIdx.x / 128;
+      x[k][p] = ml[i];
+      o[k][p] = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(i) * DC + threadIdx.x % 128 * 4);
+    }
+  const Rec r = reinterpret_cast<const Rec*>(a.d.ws)[blockIdx.x];
+  auto add = [](float4& acc, float f, const float4& v) {
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  };
   for (int pass = 0; pass < 2; ++pass) {
     const int unit = pass ? r.cont : r.lead;
     if (unit < 0) continue;
-    const int c0 = pass ? r.cont_lead : blockIdx.x, c1 = pass ? r.cont_last : r.lead_last;
-    const bool wide = c1 - c0 + 1 > 8;
-    if (!wide && pass) continue;
-    const int k = wide ? (blockIdx.x - c0) * gridDim.y + blockIdx.y : 0;
-    const int row = wide ? k : blockIdx.y * 4 + grp;
+    const int c0 = pass ? r.cont_lead : blockIdx.x, np = (pass ? r.cont_last : r.lead_last) - c0 + 1;
     const int n = unit / a.rb, rb = unit % a.rb, rows = min(NC, a.R - rb * NC);
-    if (wide && row >= rows) continue;
-    const int np = c1 - c0 + 1;
-    const int p0 = wide ? np * grp / 4 : 0, p1 = wide ? np * (grp + 1) / 4 : row < rows ? np : 0;
-    float M = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto at = [&](int p) { return ((c0 + p) * 2 + (p == 0 ? 1 : 0)) * NC + row; };
-    for (int p = p0; p < p1; ++p) M = fmaxf(M, ml[at(p)].x);
-#pragma unroll 8
-    for (int p = p0; p < p1; ++p) {
-      const float2 x = ml[at(p)];
-      const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
-      const float4 o = __ldcs(reinterpret_cast<const float4*>(part + static_cast<int64_t>(at(p)) * DC) + th);
-      l += x.y != x.y ? x.y : f * x.y;  // NaN: a page out of range
-      acc.x += f * o.x;
-      acc.y += f * o.y;
-      acc.z += f * o.z;
-      acc.w += f * o.w;
-    }
-    if (wide) {
-      acc_s[grp][th] = acc;
-      if (th == 0) {
-        ml_s[grp][0] = M;
-        ml_s[grp][1] = l;
+    const int64_t row0 = static_cast<int64_t>(n) * a.R + rb * NC;
+    auto at = [&](int p, int row) { return ((c0 + p) * 2 + (p == 0 ? 1 : 0)) * NC + row; };
+    if (kPairs && np == 2) {
+      if (pass) continue;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int row = blockIdx.y * kJoinRows + k * 4 + threadIdx.x / 128;
+        if (row >= rows) continue;
+        const float M = fmaxf(x[k][0].x, x[k][1].x);
+        const float f0 = weight(x[k][0].x, M), f1 = weight(x[k][1].x, M);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        add(acc, f0, o[k][0]);
+        add(acc, f1, o[k][1]);
+        put_row(a, row0 + row, threadIdx.x % 128 * 4, acc, M, share(f0, x[k][0].y) + share(f1, x[k][1].y));
       }
-      __syncthreads();
-      M = fmaxf(fmaxf(ml_s[0][0], ml_s[1][0]), fmaxf(ml_s[2][0], ml_s[3][0]));
-      l = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int g = 0; g < 4; ++g) {
-        const float f = ml_s[g][0] == -INFINITY ? 0.f : exp2f(ml_s[g][0] - M);
-        const float gl = ml_s[g][1];
-        l += gl != gl ? gl : f * gl;
-        const float4 o = acc_s[g][th];
-        acc.x += f * o.x;
-        acc.y += f * o.y;
-        acc.z += f * o.z;
-        acc.w += f * o.w;
-      }
-      __syncthreads();
-      if (grp != 0) continue;
-    } else if (row >= rows) {
       continue;
     }
-    const float mul = l == 0.f ? 0.f : 1.f / l;
-    const int64_t o = static_cast<int64_t>(n) * a.R + rb * NC + row;
-    const bool nan = l != l;  // poisons rows whose partials were not
-    *reinterpret_cast<uint2*>(a.d.out + o * DC + 4 * th) =
-        nan ? make_uint2(0x7fff7fffu, 0x7fff7fffu)
-            : make_uint2(pack2(acc.x * mul, acc.y * mul), pack2(acc.z * mul, acc.w * mul));
-    if (th == 0 && a.d.lse != nullptr)
-      a.d.lse[o] = nan ? l : l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    const bool by_warp = np <= 64;
+    const int b = (blockIdx.x - c0) * gridDim.y + blockIdx.y, blocks = np * gridDim.y;
+    for (int item = by_warp ? b * 16 + warp : b; item < rows * 4; item += by_warp ? blocks * 16 : blocks) {
+      const int row = item / 4, ch = item % 4 * 128 + lane * 4, step = by_warp ? 1 : 16;
+      float M = -INFINITY, l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int p0 = by_warp ? 0 : warp;
+      for (int p = p0 + step * lane; p < np; p += step * 32) M = fmaxf(M, ml[at(p, row)].x);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll 8
+      for (int p = p0; p < np; p += step) {
+        const float2 y = ml[at(p, row)];
+        const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(at(p, row)) * DC + ch);
+        const float f = weight(y.x, M);
+        l += share(f, y.y);
+        add(acc, f, v);
+      }
+      if (by_warp) {
+        put_row(a, row0 + row, ch, acc, M, l);
+        continue;
+      }
+      acc_s[warp][lane] = acc;
+      if (lane == 0) ml_s[warp] = make_float2(M, l);
+      __syncthreads();
+      if (warp == 0) {
+        for (int g = 0; g < 16; ++g) M = fmaxf(M, ml_s[g].x);
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int g = 0; g < 16; ++g) {
+          const float f = weight(ml_s[g].x, M);
+          l += share(f, ml_s[g].y);
+          add(acc, f, acc_s[g][lane]);
+        }
+        put_row(a, row0 + row, ch, acc, M, l);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -829,7 +867,7 @@ cudaError_t launch(const DecodeLatentArgs& d, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, NC / 4);
+  cfg.gridDim = dim3(grid, NC / kJoinRows);
   cfg.blockDim = dim3(512);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
