@@ -152,6 +152,7 @@ struct Roles {
   static constexpr int kThreads = 128 + 128 * kSoft + 256 * kSets;
   static constexpr int kRegs = 512 / (kThreads / 128) / 8 * 8;  // at launch
   static constexpr int kR0 = 72, kRs = NC == 64 ? 104 : 120, kRc = NC == 64 ? 96 : 72;
+  static_assert(!F8 || (kR0 <= kRegs && kRs >= kRegs && kRc <= kRegs), "");
   static_assert(!F8 || kR0 + kRs * kSoft + kRc * 2 * kSets <= kRegs * (kThreads / 128), "");
 };
 
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < 10; ++i) {
-      mbar_init(full + i, F8 ? 8 : 1);
+      mbar_init(full + i, F8 && i % kGroups < 4 ? 8 : 1);
       mbar_init(empty + i, 1);
     }
     mbar_init(s_full, 1);
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     bad_tile[0] = bad_tile[1] = 0;
     rec->cont = rec->lead = -1;
     tma_prefetch_desc(&maps.q);
-    if (!F8) tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.x);
   }
   if (warp == 1) {
     tmem_alloc(tmem, kCols);
@@ -292,8 +293,8 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
             tma_load_2d(sm + S::Q + lane * NC * 128, &maps.q, q_full, lane * 64,
                         wk.sn * a.R + wk.srb * NC);
         };
-        if (F8 || seg == 0) load_q();
-        for (int i = 0; !F8 && i < wk.cnt; ++i, ++t) {
+        if (seg == 0) load_q();
+        for (int i = 0; i < wk.cnt; ++i, ++t) {
           const int s = t & 1;
           const int pos = (wk.st + i) * KT + lane * pr;
           int64_t page = 0;
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
           const int row = static_cast<int>(page * ps + pos % ps);
           const int y = __shfl_sync(0xffffffffu, row, lane >> 1 & 3);
   #pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
+          for (int g = F8 ? 4 : 0; g < kGroups; ++g) {
             if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
             if (bailed(bail)) continue;
             uint64_t* f = full + s * kGroups + g;
@@ -315,15 +316,15 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
             const int atom = 2 * g + (lane & 1);
             if (lane < 2 * nb && atom < kAtoms)
               tma_load_2d(sm + S::X + s * kStage + atom * kAtom + (lane >> 1) * pr * 128, &maps.x, f,
-                          atom * 64, y);
+                          F8 ? kPe8 / 2 : atom * 64, y);
           }
           if (seg > 0 && i == 0) load_q();
         }
       }
       if (bailed(bail)) {  // let the copies in flight land before the CTA ends
         if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, 20000000LL);
-        for (int k = t > 2 ? t - 2 : 0; k < t && !F8; ++k)
-          for (int g = 0; g < kGroups; ++g)
+        for (int k = t > 2 ? t - 2 : 0; k < t; ++k)
+          for (int g = F8 ? 4 : 0; g < kGroups; ++g)
             mbar_wait(full + (k & 1) * kGroups + g, k / 2 & 1, 20000000LL);
       }
     } else if (warp == 1) {
@@ -612,13 +613,12 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     // ------------------------------------------- 8-bit rows, as bf16 into the stages
     reg_dec<R::kRc>();
     // Sets of eight warps; of two, one takes the even 128-channel groups and one the odd ones
-    // and k_pe. Four threads a row; of a group one takes the codes 16 q .. and 64 + 16 q .., so that
-    // 8 threads' stores touch all banks. A group's registers are refilled with the next tile's
-    // codes as soon as they are converted, so ~40 KB an SM are in flight; the block table is
+    // (k_pe is copied as it is, by TMA). Four threads a row; of a group one takes the codes
+    // 16 q .. and 64 + 16 q .., so that 8 threads' stores touch all banks. A group's registers
+    // are refilled with the next tile's codes as soon as they are converted; the block table is
     // read a tile further ahead.
     constexpr int kSets = R::kSets, kMine = 4 / (kSets > 0 ? kSets : 1);  // groups of a set
     const int i = tid - 128 - 128 * R::kSoft, set = i / 256, row = i % 256 / 4, qd = i % 4;
-    const bool last_set = set == kSets - 1;
     Walk ahead = wk;
     int left = n_tiles, in_seg = 0;
     ahead.cnt = 0;
@@ -648,41 +648,30 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     auto ld = [&](const unsigned char* p, int off) {
       return p != nullptr ? __ldg(reinterpret_cast<const uint4*>(p + off)) : zero;
     };
-    uint4 code[kMine][2], pe[2];
-    uint32_t ex = 0;
-    Row r0 = fetch();
-    const unsigned char* cur = place(r0);
-    bool bad = cur == nullptr && r0.off >= 0;
-    Row nxt = fetch();
+    uint4 code[kMine][2];
     auto load = [&](const unsigned char* p, int k) {  // group kSets k + set
 #pragma unroll
       for (int h = 0; h < 2; ++h) code[k][h] = ld(p, (kSets * k + set) * 128 + h * 64 + qd * 16);
     };
-    auto load_rest = [&](const unsigned char* p) {
-      if (last_set) {
-        pe[0] = ld(p, kPe8 + qd * 32);
-        pe[1] = ld(p, kPe8 + qd * 32 + 16);
-      }
-      if (p != nullptr) ex = __ldg(reinterpret_cast<const uint32_t*>(p + kExp8));
+    auto load_ex = [&](const unsigned char* p) {
+      return p != nullptr ? __ldg(reinterpret_cast<const uint32_t*>(p + kExp8)) : 0;
     };
+    const Row r0 = fetch();
+    const unsigned char* const p0 = place(r0);
+    bool bad = p0 == nullptr && r0.off >= 0;
+    Row nxt = fetch();
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) load(cur, k);
-    load_rest(cur);
+    for (int k = 0; k < kMine; ++k) load(p0, k);
+    uint32_t ex = load_ex(p0);
     const uint32_t sw = row & 7;
     unsigned char* const row_at = sm + S::X + (row >> 3) * 1024 + sw * 128;
     for (int t = 0; t < n_tiles; ++t) {
       const int s = t & 1;
-      const unsigned char* np = place(nxt);
+      const unsigned char* const np = place(nxt);
       const bool nbad = np == nullptr && nxt.off >= 0;
       nxt = fetch();
       unsigned char* const dst = row_at + s * kStage;
       if (bad) bad_tile[s] = t + 1;
-      const uint32_t par = (t / 2 - 1) & 1;
-      auto done = [&](int g) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full + s * kGroups + g);
-      };
 #pragma unroll
       for (int k = 0; k < kMine; ++k) {
         const int g = kSets * k + set;
@@ -690,23 +679,18 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) values16(code[k][h], ex >> (8 * g) & 0xffu, v[h]);
         load(np, k);
-        if (t >= 2) wait_for(empty + s * kGroups + g, par, bail);
+        if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             *reinterpret_cast<uint4*>(dst + (2 * g + h) * kAtom + ((qd * 2 + j) ^ sw) * 16) =
                 make_uint4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
-        done(g);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + s * kGroups + g);
       }
-      if (last_set) {
-        if (t >= 2) wait_for(empty + s * kGroups + 4, par, bail);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<uint4*>(dst + 8 * kAtom + ((qd * 2 + j) ^ sw) * 16) = pe[j];
-        done(4);
-      }
-      load_rest(np);
+      ex = load_ex(np);
       bad = nbad;
     }
   }
@@ -852,8 +836,9 @@ cudaError_t launch(const DecodeLatentArgs& d, cudaStream_t st) {
     const uint32_t box[2] = {64, NC};
     if (!make_tensor_map(&m.q, d.q, 2, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  if (!F8 && rows > 0) {
-    const uint64_t dims[2] = {DX, static_cast<uint64_t>(rows)}, strides[1] = {DX * 2};
+  if (rows > 0) {  // of an 8-bit cache: k_pe, copied as it is
+    const uint64_t pitch = F8 ? kRow8 : DX * 2;
+    const uint64_t dims[2] = {pitch / 2, static_cast<uint64_t>(rows)}, strides[1] = {pitch};
     const uint32_t box[2] = {64, static_cast<uint32_t>(d.c.page_size < KT ? d.c.page_size : KT)};
     if (!make_tensor_map(&m.x, d.c.cache, 2, dims, strides, box)) return cudaErrorInvalidValue;
   }
