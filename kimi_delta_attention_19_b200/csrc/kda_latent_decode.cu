@@ -148,10 +148,11 @@ __device__ __forceinline__ void values16(const uint4& code, uint32_t be, uint32_
 // thread: of the first warpgroup, the softmax ones and the converting ones (8-bit caches).
 template <int NC, bool F8>
 struct Roles {
-  static constexpr int kSoft = NC == 64 ? 2 : 1, kSets = !F8 ? 0 : NC == 64 ? 1 : 2;
+  static constexpr int kSoft = NC == 64 ? 2 : 1, kSets = F8 ? 2 : 0;
   static constexpr int kThreads = 128 + 128 * kSoft + 256 * kSets;
   static constexpr int kRegs = 512 / (kThreads / 128) / 8 * 8;  // at launch
-  static constexpr int kR0 = 72, kRs = NC == 64 ? 104 : 120, kRc = NC == 64 ? 96 : 72;
+  static constexpr int kR0 = NC == 64 ? 56 : 72, kRs = NC == 64 ? 96 : 120,
+                       kRc = NC == 64 ? 64 : 72;
   static_assert(!F8 || (kR0 <= kRegs && kRs >= kRegs && kRc <= kRegs), "");
   static_assert(!F8 || kR0 + kRs * kSoft + kRc * 2 * kSets <= kRegs * (kThreads / 128), "");
 };
