@@ -708,8 +708,8 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
 // over the CTAs of a unit, in their order. Usually those are two: sixteen rows a block, the
 // partials of its CTA and the next fetched before it is known whether they belong together (the
 // kernel is a chain of memory latencies). Another unit is shared by the blocks of all of
-// them: a (row, quarter of the channels) is a warp's work, or a block's from 65 CTAs on, its
-// partials spread over the block's 16 warps and summed in the warps' order.
+// them: half a row is a warp's work; from 33 CTAs on a quarter row is a block's, its partials
+// spread over the block's 16 warps and summed in the warps' order.
 constexpr int kJoinRows = 16;
 
 __device__ __forceinline__ void put_row(const Args& a, int64_t row, int ch, float4 acc, float M, float l) {
@@ -727,7 +727,7 @@ __device__ __forceinline__ float weight(float m, float M) { return m == -INFINIT
 __device__ __forceinline__ float share(float f, float l) { return l != l ? l : f * l; }  // NaN: a bad page
 
 template <int NC>
-__global__ void __launch_bounds__(512) join_kernel(const Args a) {
+__global__ void __launch_bounds__(512, NC == 64 ? 2 : 1) join_kernel(const Args a) {
   const Layout wl = ws_layout(NC);
   const float2* ml = reinterpret_cast<const float2*>(a.d.ws + wl.ml);
   const float* part = reinterpret_cast<const float*>(a.d.ws + wl.part);
@@ -777,27 +777,57 @@ __global__ void __launch_bounds__(512) join_kernel(const Args a) {
       }
       continue;
     }
-    const bool by_warp = np <= 64;
     const int b = (blockIdx.x - c0) * gridDim.y + blockIdx.y, blocks = np * gridDim.y;
-    for (int item = by_warp ? b * 16 + warp : b; item < rows * 4; item += by_warp ? blocks * 16 : blocks) {
-      const int row = item / 4, ch = item % 4 * 128 + lane * 4, step = by_warp ? 1 : 16;
+    if (np <= 32) {
+      for (int item = b * 16 + warp; item < rows * 2; item += blocks * 16) {
+        const int row = item / 2, ch = item % 2 * 256 + lane * 4;
+        const float2 y = lane < np ? ml[at(lane, row)] : make_float2(-INFINITY, 0.f);
+        float M, f = 0.f, l = 0.f;
+        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int p0 = 0; p0 < np; p0 += 4) {
+          float4 v[4][2];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float* src = part + static_cast<int64_t>(at(min(p0 + p, np - 1), row)) * DC + ch;
+            v[p][0] = *reinterpret_cast<const float4*>(src);
+            v[p][1] = *reinterpret_cast<const float4*>(src + 128);
+          }
+          if (p0 == 0) {  // weights and their sum, while the first four are on their way
+            M = y.x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            f = weight(y.x, M);
+            l = share(f, y.y);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+          }
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float fp = __shfl_sync(0xffffffffu, f, (p0 + p) & 31);
+            if (p0 + p >= np) continue;
+            add(acc[0], fp, v[p][0]);
+            add(acc[1], fp, v[p][1]);
+          }
+        }
+        put_row(a, row0 + row, ch, acc[0], M, l);
+        put_row(a, row0 + row, ch + 128, acc[1], M, l);
+      }
+      continue;
+    }
+    for (int item = b; item < rows * 4; item += blocks) {
+      const int row = item / 4, ch = item % 4 * 128 + lane * 4;
       float M = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int p0 = by_warp ? 0 : warp;
-      for (int p = p0 + step * lane; p < np; p += step * 32) M = fmaxf(M, ml[at(p, row)].x);
+      for (int p = warp + 16 * lane; p < np; p += 16 * 32) M = fmaxf(M, ml[at(p, row)].x);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-#pragma unroll 8
-      for (int p = p0; p < np; p += step) {
+#pragma unroll 5
+      for (int p = warp; p < np; p += 16) {
         const float2 y = ml[at(p, row)];
         const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(at(p, row)) * DC + ch);
         const float f = weight(y.x, M);
         l += share(f, y.y);
         add(acc, f, v);
-      }
-      if (by_warp) {
-        put_row(a, row0 + row, ch, acc, M, l);
-        continue;
       }
       acc_s[warp][lane] = acc;
       if (lane == 0) ml_s[warp] = make_float2(M, l);
