@@ -1,0 +1,214 @@
+"""Latent attention on the GPU at the ends of its ranges: offsets past 32 bits, scores that rise
+all along a sequence, long sequences, values that are not finite, tensors made on other
+streams. Against the fp64 references of tests/latent_ref.py."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from tests import latent_ref as ref
+from tests.test_latent_gpu import DEV, cu, decode_case, expanded_inputs, paged, rnd, slots_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def latent():
+    from kimi_delta_attention_19_b200 import latent as m
+    return m
+
+
+@pytest.mark.parametrize("lq,lk,H,causal", [
+    ([2300], [2300], 2, True),
+    ([70], [3500], 3, True),                  # few queries behind a long prefix
+    ([3000], [100], 1, True),                 # most rows see nothing
+    ([1, 129], [4000, 5], 2, False),
+    ([257] * 5, [257] * 5, 7, True),
+])
+def test_longer_sequences(latent, lq, lk, H, causal):
+    q, kn, pe, v, g = expanded_inputs(lq, lk, H, seed=sum(lq))
+    kw = dict(cu_seqlens=cu(lq), cu_seqlens_k=cu(lk), max_seqlen=max(lq), max_seqlen_k=max(lk),
+              causal=causal)
+    out, lse = latent.latent_attn_fwd(q, kn, pe, v, **kw)
+    grads = latent.latent_attn_bwd(q, kn, pe, v, out, lse, g, **kw)
+    want = ref.expanded(q, kn, pe, v, lq, lk, causal, d_out=g, out_used=out)
+    ref.inside(out, want["out"], want["b_out"], "out")
+    ref.lse_close(lse, want["lse"])
+    for name, got in zip(("dq", "dk_nope", "dk_pe", "dv"), grads):
+        ref.inside(got, want[name], want["b_" + name], name)
+
+
+def test_loose_bounds_give_the_same(latent):
+    """max_seqlen only sizes the launch."""
+    lens = [100, 300, 0, 33]
+    q, kn, pe, v, g = expanded_inputs(lens, lens, 2, seed=1)
+    a = latent.latent_attn_fwd(q, kn, pe, v, cu_seqlens=cu(lens), max_seqlen=300)
+    b = latent.latent_attn_fwd(q, kn, pe, v, cu_seqlens=cu(lens))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga = latent.latent_attn_bwd(q, kn, pe, v, *a, g, cu_seqlens=cu(lens), max_seqlen=300)
+    gb = latent.latent_attn_bwd(q, kn, pe, v, *a, g, cu_seqlens=cu(lens))
+    assert all(torch.equal(x, y) for x, y in zip(ga, gb))
+
+
+def test_rising_scores(latent):
+    """Scores that grow by some units every key tile: the softmax reference is raised again and
+    again, and what came before fades to nothing. Scores reach some 200, so fp32 sums of 192
+    products err by 192 * 2^-24 * (sum of magnitudes ~ 200) ~ 2e-3 at the very worst and by its
+    root-sum some 2e-4: within the bound's room (2^-8 of p) for the keys that count."""
+    n, H = 1200, 2
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    dirn = torch.randn(192, generator=gen, device=DEV)
+    dirn = dirn / dirn.norm()
+    ramp = torch.linspace(0, 1, n, device=DEV)[:, None, None]
+    q = (60 * dirn).expand(n, H, 192).to(torch.bfloat16).contiguous()
+    k = (46 * ramp * dirn).expand(n, H, 192).to(torch.bfloat16)
+    kn, pe = k[..., :128].contiguous(), k[:, 0, 128:].contiguous()
+    v = rnd(gen, n, H, 128)
+    out, lse = latent.latent_attn_fwd(q, kn, pe, v)
+    want = ref.expanded(q, kn, pe, v, [n], [n], True)
+    assert float(want["lse"].max()) > 150
+    ref.inside(out, want["out"], want["b_out"], "out")
+    ref.lse_close(lse, want["lse"])
+    # the same over a cache, whose rows and query carry the ramp in the latent part
+    rows = torch.zeros(n, 576, dtype=torch.bfloat16, device=DEV)
+    rows[:, :192] = k[:, 0]
+    rows[:, 192:512] = rnd(gen, n, 320)
+    table, pages = paged([n], 16, seed=3)
+    cache = latent.latent_cache(pages, 16, device=DEV)
+    latent.latent_cache_write(rows[:, :512], rows[:, 512:], cache, slots_of(table, [n], 16))
+    qa = torch.zeros(1, 1, 20, 576, dtype=torch.bfloat16, device=DEV)
+    qa[..., :192] = q[0, 0]
+    o = latent.latent_decode(qa, cache, table, torch.tensor([n], dtype=torch.int32, device=DEV))
+    want, bnd, _ = ref.absorbed(qa, cache, table, [n])
+    ref.inside(o, want, bnd, "decode")
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_query_stays_in_its_row(latent, bad):
+    lens, H = [200, 90], 2
+    q, kn, pe, v, g = expanded_inputs(lens, lens, H, seed=5)
+    kw = dict(cu_seqlens=cu(lens), max_seqlen=200)
+    clean, _ = latent.latent_attn_fwd(q, kn, pe, v, **kw)
+    q[77, 1] = bad
+    out, lse = latent.latent_attn_fwd(q, kn, pe, v, **kw)
+    rest = torch.ones(q.shape[:2], dtype=torch.bool, device=DEV)
+    rest[77, 1] = False
+    assert torch.equal(out[rest], clean[rest])
+    assert torch.isnan(out[77, 1].float()).all() and not torch.isfinite(lse[77, 1])
+    x = decode_case(latent, [300, 5], 9, 1, 16, False, seed=6, garbage=False)
+    clean = latent.latent_decode(*x)
+    x[0][0, 0, 3] = bad
+    o = latent.latent_decode(*x)
+    rest = torch.ones(o.shape[:3], dtype=torch.bool, device=DEV)
+    rest[0, 0, 3] = False
+    assert torch.equal(o[rest], clean[rest]) and torch.isnan(o[0, 0, 3].float()).all()
+
+
+def test_element_offsets_past_32_bits(latent):
+    """Token strides of 32 M elements: rows more than 2^32 elements (and bytes) apart."""
+    T, H, stride = 140, 2, 1 << 25
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    base = torch.empty((T - 1) * stride + 4096, dtype=torch.bfloat16, device=DEV)
+    view = lambda d, at, step: base.as_strided((T, H, d), (stride, step, 1), at)  # noqa: E731
+    q, kn, v = view(192, 0, 192), view(128, 512, 256), view(128, 640, 256)
+    pe = base.as_strided((T, 64), (stride, 1), 2048)
+    for t in (q, kn, v, pe):
+        t.copy_(rnd(gen, *t.shape))
+    assert (T - 1) * stride > 1 << 32
+    g = rnd(gen, T, H, 128)
+    out, lse = latent.latent_attn_fwd(q, kn, pe, v)
+    grads = latent.latent_attn_bwd(q, kn, pe, v, out, lse, g)
+    near = [t.contiguous() for t in (q, kn, pe, v)]
+    want = ref.expanded(*near, [T], [T], True, d_out=g, out_used=out)
+    ref.inside(out, want["out"], want["b_out"], "out")
+    for name, got in zip(("dq", "dk_nope", "dk_pe", "dv"), grads):
+        ref.inside(got, want[name], want["b_" + name], name)
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+def test_cache_offsets_past_32_bits(latent, quantized):
+    """A cache of more than 4 GB, its last pages in use."""
+    ps, lens = 128, [300, 129]
+    n_pages = (56000 if quantized else 32000)                  # 4.7 GB
+    cache = torch.empty(n_pages, ps, 656 if quantized else 576, device=DEV,
+                        dtype=torch.uint8 if quantized else torch.bfloat16)
+    assert cache.numel() * cache.element_size() > 1 << 32
+    table = torch.tensor([[n_pages - 1, n_pages - 5, 3], [n_pages - 2, n_pages - 3, 0]],
+                         dtype=torch.int32, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    T = sum(lens)
+    c, pe = rnd(gen, T, 512), rnd(gen, T, 64)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    latent.latent_cache_write(c, pe, cache, slots_of(table, lens, ps), status=st)
+    back = latent.latent_cache_read(cache, table, cu(lens), total=T, status=st)
+    want = ref.quantize(c)[0] if quantized else c.double()
+    assert torch.equal(back[:, :512].double(), want) and torch.equal(back[:, 512:], pe)
+    q = rnd(gen, 2, 1, 32, 576)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = latent.latent_decode(q, cache, table, sl, status=st)
+    # the same rows in a small cache give the same bits
+    small, pages = paged(lens, ps, seed=9)
+    near = latent.latent_cache(pages, ps, quantized=quantized, device=DEV)
+    latent.latent_cache_write(c, pe, near, slots_of(small, lens, ps))
+    assert torch.equal(out, latent.latent_decode(q, near, small, sl))
+    assert int(st) == 0
+
+
+def test_padded_batch_of_queries_and_empty_sequences(latent):
+    """A serving batch padded with length-0 sequences and skipped slots."""
+    lens = [0, 700, 0, 0, 33, 0]
+    q, cache, table, sl = decode_case(latent, lens, 32, 1, 64, True, seed=10)
+    lse = torch.empty(q.shape[:3], device=DEV)
+    out = latent.latent_decode(q, cache, table, sl, lse=lse)
+    want, bnd, wl = ref.absorbed(q, cache, table, lens)
+    ref.inside(out, want, bnd, "out")
+    assert (out[[0, 2, 3, 5]] == 0).all() and (lse[[0, 2, 3, 5]] == -math.inf).all()
+    # a table of no columns, a cache of no pages: every sequence of length 0 is empty
+    none = latent.latent_cache(0, 16, device=DEV)
+    zero = torch.zeros(6, dtype=torch.int32, device=DEV)
+    out = latent.latent_decode(q, none, torch.zeros(6, 0, dtype=torch.int32, device=DEV), zero)
+    assert (out == 0).all()
+
+
+def test_inputs_made_on_another_stream(latent):
+    """The call runs on the given stream, behind what that stream made."""
+    lens = [500, 77]
+    q, kn, pe, v, g = expanded_inputs(lens, lens, 2, seed=11)
+    kw = dict(cu_seqlens=cu(lens), max_seqlen=500)
+    want, _ = latent.latent_attn_fwd(q * 2, kn, pe, v, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        big = torch.randn(4096, 4096, device=DEV)
+        for _ in range(20):                                    # keeps the stream busy
+            big = (big @ big).clamp(-1, 1)
+        q2 = q * 2
+    out, lse = latent.latent_attn_fwd(q2, kn, pe, v, stream=side, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want)
+
+
+def test_two_captured_decodes_interleaved(latent):
+    """Graphs with workspaces of their own, replayed in any order and beside eager calls."""
+    cases = [decode_case(latent, [900, 40], 32, 1, 64, False, seed=12),
+             decode_case(latent, [50, 3000], 8, 4, 16, True, seed=13)]
+    want = [latent.latent_decode(*c) for c in cases]
+    torch.cuda.synchronize()
+    graphs = []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = latent.latent_decode(*c)
+        graphs.append((g, o))
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1)):
+        for _, o in graphs:
+            o.zero_()
+        for i in order:
+            graphs[i][0].replay()
+        eager = latent.latent_decode(*cases[0])
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[0])
+        for i in set(order):
+            assert torch.equal(graphs[i][1], want[i])
