@@ -40,11 +40,13 @@ def _compile(src: str, obj: str, extra: list[str] | None = None) -> str:
 
 
 # Test-only variant of the library: the first wait on the inputs in each tensor-core prefill
-# kernel gives up after 64 clocks, so a test can watch the kernels' bail-out path (status
-# word set, copies and products drained, tensor memory freed) run on the GPU and the
-# context stay usable. The product never loads it.
+# kernel, and any wait in a latent-attention kernel, gives up after 64 clocks, so a test can
+# watch the kernels' bail-out path (status word set, copies and products drained, tensor memory
+# freed) run on the GPU and the context stay usable. The product never loads it.
 SHORTWAIT_LIB = os.path.join(PKG, "libkda_shortwait.so")
-SHORTWAIT_DEFINES = {"kda_prefill_tc.cu": ["-DKDA_FIRST_WAIT_LIMIT=64", "-DKDA_FIRST_WAIT_STUCK=1"]}
+SHORTWAIT_DEFINES = {"kda_prefill_tc.cu": ["-DKDA_FIRST_WAIT_LIMIT=64", "-DKDA_FIRST_WAIT_STUCK=1"],
+                     **{f"kda_latent_{k}.cu": ["-DKDA_LATENT_WAIT_CYCLES=64"]
+                        for k in ("fwd", "bwd", "decode")}}
 
 
 def _link(lib: str, objs: list[str]) -> None:

@@ -185,11 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 3; ++i) tma_load_3d(st + i * kAtomQ, &maps.qs, full + s, 64 * i, h, row);
           for (int i = 0; i < 2; ++i) tma_load_3d(st + (3 + i) * kAtomQ, &maps.douts, full + s, 64 * i, h, row);
         }
-        if (*bail) {  // let the copies in flight land before the CTA ends
-          mbar_wait(res_full, 0, 20000000LL);
-          for (int k = t > kQStages ? t - kQStages : 0; k < t; ++k)
-            mbar_wait(full + k % kQStages, k / kQStages & 1, 20000000LL);
-        }
+        mbar_wait(res_full, 0, kDrainCycles);
+        for (int k = t > kQStages ? t - kQStages : 0; k < t; ++k)
+          mbar_wait(full + k % kQStages, k / kQStages & 1, kDrainCycles);
       }
     } else if (warp == 1 && n > 0) {
       constexpr uint32_t i64 = idesc_bf16(BM, BQ, 0, 0), iv = idesc_bf16(BM, 128, 0, 1),
@@ -245,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(o_full);
         if (*bail) {
           umma_commit(drain);
-          mbar_wait(drain, 0, 20000000LL);
+          mbar_wait(drain, 0, kDrainCycles);
         }
       }
     } else if (warp == 2 && n > 0 && r.lq - (j1 - 1) * BQ < BQ) {
@@ -379,13 +377,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(sm + SmQ::V + (2 * sv + i) * kAtomQ, &maps.vs, v_full + sv, 64 * i, h, row);
           ++tv;
         }
-        if (*bail) {  // let the copies in flight land before the CTA ends
-          mbar_wait(res_full, 0, 20000000LL);
-          for (int k = t > kKStages ? t - kKStages : 0; k < t; ++k)
-            mbar_wait(full + k % kKStages, k / kKStages & 1, 20000000LL);
-          for (int k = tv > kVStages ? tv - kVStages : 0; k < tv; ++k)
-            mbar_wait(v_full + k % kVStages, k / kVStages & 1, 20000000LL);
-        }
+        mbar_wait(res_full, 0, kDrainCycles);
+        for (int k = t > kKStages ? t - kKStages : 0; k < t; ++k)
+          mbar_wait(full + k % kKStages, k / kKStages & 1, kDrainCycles);
+        for (int k = tv > kVStages ? tv - kVStages : 0; k < tv; ++k)
+          mbar_wait(v_full + k % kVStages, k / kVStages & 1, kDrainCycles);
       }
     } else if (warp == 1 && n > 0) {
       constexpr uint32_t i64 = idesc_bf16(BM, BQ, 0, 0), iq = idesc_bf16(BM, 192, 0, 1);
@@ -434,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(o_full);
         if (*bail) {
           umma_commit(drain);
-          mbar_wait(drain, 0, 20000000LL);
+          mbar_wait(drain, 0, kDrainCycles);
         }
       }
     } else if (warp == 2 && n > 0 && r.lk - (n - 1) * BQ < BQ) {

@@ -282,11 +282,13 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     if (warp == 0) {
       // ------------------------------------------------------------------ loads
       const int ps = d.c.page_size, pr = ps < KT ? ps : KT;  // rows of a box
-      int t = 0, q_loads = 0;
+      int t = 0, q_loads = 0, groups = 0;  // groups: column groups under way, in order
+      bool stop = false;
       for (int seg = 0; wk.next(a); ++seg) {
         auto load_q = [&] {
           if (seg > 0) wait_for(q_empty, (seg - 1) & 1, bail);
-          if (bailed(bail)) return;
+          stop |= bailed(bail);
+          if (stop) return;
           ++q_loads;
           if (lane == 0) mbar_arrive_expect_tx(q_full, kAtoms * NC * 128);
           __syncwarp();
@@ -303,14 +305,18 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
           if (there) page = d.table[wk.sn * d.table_pages + pos / ps];
           const bool bad = page < 0 || page >= d.c.n_pages;
           if (bad) page = 0;
-          if (__any_sync(0xffffffffu, bad) && lane == 0) bad_tile[s] = t + 1;
+          const bool any_bad = __any_sync(0xffffffffu, bad);
           const int nb = __popc(__ballot_sync(0xffffffffu, there));
           const int row = static_cast<int>(page * ps + pos % ps);
           const int y = __shfl_sync(0xffffffffu, row, lane >> 1 & 3);
   #pragma unroll
           for (int g = F8 ? 4 : 0; g < kGroups; ++g) {
             if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
-            if (bailed(bail)) continue;
+            stop |= bailed(bail);
+            if (stop) continue;
+            ++groups;
+            // (the stage's last tile has been looked at once its O^T is under way)
+            if (!F8 && g == 0 && any_bad && lane == 0) bad_tile[s] = t + 1;
             uint64_t* f = full + s * kGroups + g;
             if (lane == 0) mbar_arrive_expect_tx(f, nb * pr * (g < 4 ? 256 : 128));
             __syncwarp();
@@ -322,12 +328,10 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
           if (seg > 0 && i == 0) load_q();
         }
       }
-      if (bailed(bail)) {  // let the copies in flight land before the CTA ends
-        if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, 20000000LL);
-        for (int k = t > 2 ? t - 2 : 0; k < t; ++k)
-          for (int g = F8 ? 4 : 0; g < kGroups; ++g)
-            mbar_wait(full + (k & 1) * kGroups + g, k / 2 & 1, 20000000LL);
-      }
+      if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, kDrainCycles);
+      constexpr int kPer = F8 ? 1 : kGroups;  // groups a tile
+      for (int k = max(0, groups - 2 * kPer); k < groups; ++k)
+        mbar_wait(full + (k / kPer & 1) * kGroups + (F8 ? 4 : k % kPer), k / kPer / 2 & 1, kDrainCycles);
     } else if (warp == 1) {
       // --------------------------------------------------------- products: S^T
       // Two warps issue, so that O^T of a tile waits neither for the next tile to arrive nor for
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
         }
         if (*bail) {
           umma_commit(drain);
-          mbar_wait(drain, 0, 20000000LL);
+          mbar_wait(drain, 0, kDrainCycles);
         }
       }
     } else if (warp == 2) {
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
         }
         if (*bail) {
           umma_commit(drain + 1);
-          mbar_wait(drain + 1, 0, 20000000LL);
+          mbar_wait(drain + 1, 0, kDrainCycles);
         }
       }
     }
@@ -564,7 +568,6 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
       if (tw < NW) fac[cw] = mul;
       if (tid == 128) {
         if (bad && d.status != nullptr) atomicExch(d.status, kDevBadPage);
-        if (*bail && d.status != nullptr) atomicExch(d.status, kDevWaitTimeout);
         const int64_t u0 = gt - wk.st, u1 = u0 + wk.tiles - 1;  // the unit's first, last tile
         const int unit = wk.sn * a.rb + wk.srb;
         const int last_cta = static_cast<int>(((u1 + 1) * G - 1) / total);
@@ -672,7 +675,6 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
       const bool nbad = np == nullptr && nxt.off >= 0;
       nxt = fetch();
       unsigned char* const dst = row_at + s * kStage;
-      if (bad) bad_tile[s] = t + 1;
 #pragma unroll
       for (int k = 0; k < kMine; ++k) {
         const int g = kSets * k + set;
@@ -681,6 +683,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
         for (int h = 0; h < 2; ++h) values16(code[k][h], ex >> (8 * g) & 0xffu, v[h]);
         load(np, k);
         if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
+        if (k == 0 && bad) bad_tile[s] = t + 1;  // (the stage's last tile has been looked at)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -698,6 +701,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *bail && d.status != nullptr) atomicExch(d.status, kDevWaitTimeout);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, kCols);

@@ -110,13 +110,13 @@ __global__ void __launch_bounds__(384, 1)
       // ---------------------------------------------------------------- loads
       if (elect_one()) {
         int c = 0;
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; j < n && !*bail; ++j) {
           const int row = static_cast<int>(r.k0) + j * BN;
 #pragma unroll
           for (int i = 0; i < kPerTile; ++i, ++c) {
             const int s = c % kRing;
             if (c >= kRing) wait_for(empty + s, (c / kRing - 1) & 1, bail);
-            if (*bail) continue;
+            if (*bail) break;
             mbar_arrive_expect_tx(full + s, kAtom);
             unsigned char* dst = sm + Sm::RING + s * kAtom;
             if (i < 2) tma_load_3d(dst, &maps.kn, full + s, 64 * i, h, row);
@@ -124,12 +124,10 @@ __global__ void __launch_bounds__(384, 1)
             else tma_load_3d(dst, &maps.v, full + s, 64 * (i - 3), h, row);
           }
         }
-        if (*bail) {  // let the copies in flight land before the CTA ends
-          for (int g = 0; g < 2; ++g)
-            if (nk[g] > 0) mbar_wait(q_full + g, 0, 20000000LL);
-          for (int k = c > kRing ? c - kRing : 0; k < c; ++k)
-            mbar_wait(full + k % kRing, k / kRing & 1, 20000000LL);
-        }
+        for (int g = 0; g < 2; ++g)
+          if (nk[g] > 0) mbar_wait(q_full + g, 0, kDrainCycles);
+        for (int k = c > kRing ? c - kRing : 0; k < c; ++k)
+          mbar_wait(full + k % kRing, k / kRing & 1, kDrainCycles);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------- products
@@ -198,7 +196,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (*bail) {
           umma_commit(drain);
-          mbar_wait(drain, 0, 20000000LL);
+          mbar_wait(drain, 0, kDrainCycles);
         }
       }
     } else if (warp == 2 && n > 0 && r.lk - (n - 1) * BN < BN) {
@@ -348,11 +346,11 @@ __global__ void __launch_bounds__(384, 1)
     const int first = i0 + g * BM + w * 32;  // this warp's rows
     copy_rows<2>(tile, reinterpret_cast<unsigned char*>(a.out + ((r.q0 + first) * a.H + h) * DV),
                  static_cast<int64_t>(a.H) * DV * 2, w * 32, min(32, r.lq - first), 0, 1, lane);
-    if (tid == 128 && *bail && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *bail && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, 512);

@@ -37,9 +37,13 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 
 // Bounded waits. `bail` is a shared word of the CTA: the first wait that runs out (about a
 // second) sets it, every later wait returns at once, no further copy is issued, and all loops
-// run to their ends (so no named barrier is left short); the kernel then waits for what it has
-// in flight, reports kDevWaitTimeout and frees its tensor memory.
-constexpr long long kWaitCycles = 2000000000LL;
+// run to their ends (so no named barrier is left short); the CTA then waits (again with a limit)
+// for its products in flight, reports kDevWaitTimeout and frees its tensor memory. The loading
+// thread always waits for its last copies before it is done, whatever became of the others.
+#ifndef KDA_LATENT_WAIT_CYCLES  // (the test-only library gives up almost at once)
+#define KDA_LATENT_WAIT_CYCLES 2000000000LL
+#endif
+constexpr long long kWaitCycles = KDA_LATENT_WAIT_CYCLES, kDrainCycles = 100000000LL;
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* bail) {
   if (mbar_try_wait(bar, parity)) return;
   const long long t0 = clock64();

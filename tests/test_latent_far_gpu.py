@@ -212,3 +212,19 @@ def test_two_captured_decodes_interleaved(latent):
         assert torch.equal(eager, want[0])
         for i in set(order):
             assert torch.equal(graphs[i][1], want[i])
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+def test_every_sequence_of_a_full_batch_has_a_bad_page(latent, quantized):
+    """One-tile sequences, several a thread block: each is reported by itself, the good ones
+    between them are not."""
+    n = 700
+    lens = [64] * n
+    q, cache, table, sl = decode_case(latent, lens, 4, 1, 64, quantized, seed=14)
+    good = latent.latent_decode(q, cache, table, sl)
+    bad = torch.arange(n, device=DEV) % 7 != 3
+    table[bad, 0] = cache.shape[0] + 5
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = latent.latent_decode(q, cache, table, sl, status=st)
+    assert latent.status_of(st) == (4, 3)
+    assert torch.isnan(out[bad].float()).all() and torch.equal(out[~bad], good[~bad])
