@@ -1,9 +1,11 @@
-"""Build libkda.so (the C-ABI CUDA library) in-tree for sm_100a.
+"""Build libkda.so (the C-ABI CUDA library) in-tree for sm_100a, and the latent-attention
+binding's extension module.
 
     python -m kimi_delta_attention_19_b200.build
 
 Each .cu under csrc/ is compiled by nvcc in parallel into _build/, then linked
-into kimi_delta_attention_19_b200/libkda.so. Nothing is JIT-compiled at import.
+into kimi_delta_attention_19_b200/libkda.so; csrc/latent_host.cpp becomes
+_latent_host.so beside it. Nothing is JIT-compiled at import.
 """
 from __future__ import annotations
 
@@ -56,6 +58,31 @@ def _link(lib: str, objs: list[str]) -> None:
     subprocess.run(cmd, check=True)
 
 
+# The latent-attention binding's extension module (csrc/latent_host.cpp), for this interpreter
+# and this torch.
+HOST_MODULE = os.path.join(PKG, "_latent_host.so")
+
+
+def _build_host(src: str) -> str:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    libs = os.path.join(root, "lib")
+    cuda_home = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda_home, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{i}" for i in inc), src, "-o", HOST_MODULE, f"-L{libs}",
+           f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    return r.stderr
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -80,6 +107,10 @@ def build(verbose: bool = False) -> str:
                 if os.path.exists(o) and os.path.getmtime(o) >= newest_dep:
                     continue
                 jobs[ex.submit(_compile, src, o, extra)] = (name, extra)
+        host_src = os.path.join(CSRC, "latent_host.cpp")
+        if not os.path.exists(HOST_MODULE) or os.path.getmtime(HOST_MODULE) < max(
+                os.path.getmtime(host_src), os.path.getmtime(os.path.join(ROOT, "include", "kda.h"))):
+            jobs[ex.submit(_build_host, host_src)] = ("latent_host.cpp", [])
         for fut in cf.as_completed(jobs):
             report = fut.result()
             if verbose:

@@ -34,7 +34,7 @@ namespace {
 constexpr int BM = 128;                    // queries of a dQ CTA, keys of a dK CTA
 constexpr int BQ = 64;                     // query step of a dK CTA, key step of a dQ CTA
 constexpr uint32_t kAtom = BM * 128, kAtomQ = BQ * 128;
-constexpr int kFew = 256;                  // keys up to which dS is kept in two terms
+constexpr int kFew = 128;                  // keys up to which dS is kept in two terms
 constexpr int kQStages = 3, kKStages = 4, kVStages = 3;
 constexpr int kThreads = 384, kSoft = 256;
 

@@ -99,6 +99,17 @@ def _bf16(t: torch.Tensor, name: str, index: int) -> None:
         raise ValueError(f"{name} is on {t.device}, the other tensors are not")
 
 
+# The usual calls (current device and stream, results allocated here, no status word) go through
+# an extension module; where that answers None, or is not built, the checks below run and say
+# what is wrong.
+try:
+    from . import _latent_host as _host
+    _host.bind(*(ctypes.cast(getattr(lib, "kda_latent_" + n), ctypes.c_void_p).value
+                 for n in ("attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "cache_write",
+                           "cache_read", "decode", "decode_workspace_size")))
+except ImportError:
+    _host = None
+
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
     else lambda index: torch.cuda.current_stream(index).cuda_stream
 
@@ -204,6 +215,11 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v
     """
     if cu_seqlens is not None and cu_seqlens_k is None:
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
+    if _host is not None and stream is None and out is None and lse is None and status is None:
+        r = _host.attn_fwd(q, k_nope, k_pe, v, cu_seqlens, cu_seqlens_k, max_seqlen, max_seqlen_k,
+                           causal, scale)
+        if r is not None:
+            return r
     at = q.get_device()
     if _elsewhere(at, stream):
         with _there(at, stream):
@@ -243,6 +259,12 @@ def latent_attn_bwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v
     and latent_attn_fwd."""
     if cu_seqlens is not None and cu_seqlens_k is None:
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
+    if _host is not None and stream is None and grads is None and workspace is None \
+            and status is None:
+        r = _host.attn_bwd(q, k_nope, k_pe, v, cu_seqlens, cu_seqlens_k, max_seqlen, max_seqlen_k,
+                           causal, scale, out, lse, d_out)
+        if r is not None:
+            return r
     at = q.get_device()
     if _elsewhere(at, stream):
         with _there(at, stream):
@@ -353,6 +375,9 @@ def latent_cache_write(latent: torch.Tensor, k_pe: torch.Tensor, cache: torch.Te
     strided) to rows slots [T] (int64: page * page_size + offset). Negative slots are
     skipped (padding); one past the cache is skipped and reported as 3 in `status` (int32
     device tensor). Slots must be distinct."""
+    if _host is not None and stream is None and status is None:
+        if _host.cache_write(latent, k_pe, cache, slots):
+            return
     at = cache.get_device()
     if _elsewhere(at, stream):
         with _there(at, stream):
@@ -380,6 +405,10 @@ def latent_cache_read(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens
     then k_pe), for instance to expand a cached prefix in front of new queries. block_table
     is int32 [n, pages]. A token past its table or with a page out of range is NaN and
     reported as 3 in `status`; rows behind the last sequence are not written."""
+    if _host is not None and stream is None and out is None and starts is None and status is None:
+        r = _host.cache_read(cache, block_table, cu_seqlens, total)
+        if r is not None:
+            return r
     at = cache.get_device()
     if _elsewhere(at, stream):
         with _there(at, stream):
@@ -428,6 +457,11 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     out = 0, lse = -inf. seq_lens past the table or a page out of range: NaN rows and 3 in
     `status`. `workspace` may be kept (latent_decode_workspace); it serves one call at a time.
     """
+    if _host is not None and stream is None and out is None and lse is None \
+            and workspace is None and status is None:
+        r = _host.decode(q, cache, block_table, seq_lens, draft_mask, scale)
+        if r is not None:
+            return r
     at = cache.get_device()
     if _elsewhere(at, stream):
         with _there(at, stream):
