@@ -139,6 +139,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n = j1 - j0;
 
+  if (warp == 2 && n > 0) {
+    if (is_k && lane < 5)
+      tma_prefetch_desc(lane == 0 ? &maps.kn : lane == 1 ? &maps.kp : lane == 2 ? &maps.v
+                        : lane == 3 ? &maps.qs : &maps.douts);
+    if (!is_k && lane < 5)
+      tma_prefetch_desc(lane == 0 ? &maps.q : lane == 1 ? &maps.dout : lane == 2 ? &maps.kns
+                        : lane == 3 ? &maps.kps : &maps.vs);
+  }
+  // step t's rows into their stage
+  auto load_queries = [&](int t) {
+    const int s = t % kQStages, row = static_cast<int>(r.q0) + (j0 + t) * BQ;
+    unsigned char* st = sm + SmK::ST + s * SmK::STAGE;
+    mbar_arrive_expect_tx(full + s, SmK::STAGE);
+    for (int i = 0; i < 3; ++i) tma_load_3d(st + i * kAtomQ, &maps.qs, full + s, 64 * i, h, row);
+    for (int i = 0; i < 2; ++i) tma_load_3d(st + (3 + i) * kAtomQ, &maps.douts, full + s, 64 * i, h, row);
+  };
+  auto load_keys = [&](int t) {
+    const int s = t % kKStages, row = static_cast<int>(r.k0) + t * BQ;
+    unsigned char* st = sm + SmQ::K + s * 3 * kAtomQ;
+    mbar_arrive_expect_tx(full + s, 3 * kAtomQ);
+    for (int i = 0; i < 2; ++i) tma_load_3d(st + i * kAtomQ, &maps.kns, full + s, 64 * i, h, row);
+    tma_load_2d(st + 2 * kAtomQ, &maps.kps, full + s, 0, row);
+  };
+  auto load_values = [&](int t) {
+    const int s = t % kVStages, row = static_cast<int>(r.k0) + t * BQ;
+    mbar_arrive_expect_tx(v_full + s, 2 * kAtomQ);
+    for (int i = 0; i < 2; ++i)
+      tma_load_3d(sm + SmQ::V + (2 * s + i) * kAtomQ, &maps.vs, v_full + s, 64 * i, h, row);
+  };
   if (tid == 0) {
     for (int i = 0; i < 14; ++i) mbar_init(bar + i, 1);  // stages, full and empty
     mbar_init(res_full, 1);
@@ -156,17 +185,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(fixed, 32);
     fence_mbar_init();
     *bail = 0;
-    if (n > 0) {  // the CTA's own rows, on their way while it sets up
+    if (n > 0) {  // the CTA's own rows and the first step's, on their way while it sets up
       mbar_arrive_expect_tx(res_full, 5 * kAtom);
       if (is_k) {
         const int row = static_cast<int>(r.k0) + b0;
         for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmK::K + i * kAtom, &maps.kn, res_full, 64 * i, h, row);
         tma_load_2d(sm + SmK::K + 2 * kAtom, &maps.kp, res_full, 0, row);
         for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmK::V + i * kAtom, &maps.v, res_full, 64 * i, h, row);
+        load_queries(0);
       } else {
         const int row = static_cast<int>(r.q0) + b0;
         for (int i = 0; i < 3; ++i) tma_load_3d(sm + SmQ::Q + i * kAtom, &maps.q, res_full, 64 * i, h, row);
         for (int i = 0; i < 2; ++i) tma_load_3d(sm + SmQ::DO + i * kAtom, &maps.dout, res_full, 64 * i, h, row);
+        load_keys(0);
+        load_values(0);
       }
     }
   }
@@ -189,15 +221,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp == 0) {
       if (n > 0 && elect_one()) {
-        int t = 0;
+        int t = 1;
         for (; t < n; ++t) {
-          const int s = t % kQStages, row = static_cast<int>(r.q0) + (j0 + t) * BQ;
-          if (t >= kQStages) wait_for(empty + s, (t / kQStages - 1) & 1, bail);
+          if (t >= kQStages) wait_for(empty + t % kQStages, (t / kQStages - 1) & 1, bail);
           if (*bail) break;
-          unsigned char* st = sm + SmK::ST + s * SmK::STAGE;
-          mbar_arrive_expect_tx(full + s, SmK::STAGE);
-          for (int i = 0; i < 3; ++i) tma_load_3d(st + i * kAtomQ, &maps.qs, full + s, 64 * i, h, row);
-          for (int i = 0; i < 2; ++i) tma_load_3d(st + (3 + i) * kAtomQ, &maps.douts, full + s, 64 * i, h, row);
+          load_queries(t);
         }
         mbar_wait(res_full, 0, kDrainCycles);
         for (int k = t > kQStages ? t - kQStages : 0; k < t; ++k)
@@ -389,20 +417,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool few = (a.causal ? min(r.lk, b0 + BM + lag) : r.lk) <= kFew;
     if (warp == 0) {
       if (n > 0 && elect_one()) {
-        int t = 0, tv = 0;
+        int t = 1, tv = 1;
         for (; t < n; ++t) {
-          const int s = t % kKStages, sv = t % kVStages, row = static_cast<int>(r.k0) + t * BQ;
-          if (t >= kKStages) wait_for(empty + s, (t / kKStages - 1) & 1, bail);
+          if (t >= kKStages) wait_for(empty + t % kKStages, (t / kKStages - 1) & 1, bail);
           if (*bail) break;
-          unsigned char* st = sm + SmQ::K + s * 3 * kAtomQ;
-          mbar_arrive_expect_tx(full + s, 3 * kAtomQ);
-          for (int i = 0; i < 2; ++i) tma_load_3d(st + i * kAtomQ, &maps.kns, full + s, 64 * i, h, row);
-          tma_load_2d(st + 2 * kAtomQ, &maps.kps, full + s, 0, row);
-          if (t >= kVStages) wait_for(v_empty + sv, (t / kVStages - 1) & 1, bail);
+          load_keys(t);
+          if (t >= kVStages) wait_for(v_empty + t % kVStages, (t / kVStages - 1) & 1, bail);
           if (*bail) { ++t; break; }
-          mbar_arrive_expect_tx(v_full + sv, 2 * kAtomQ);
-          for (int i = 0; i < 2; ++i)
-            tma_load_3d(sm + SmQ::V + (2 * sv + i) * kAtomQ, &maps.vs, v_full + sv, 64 * i, h, row);
+          load_values(t);
           ++tv;
         }
         mbar_wait(res_full, 0, kDrainCycles);

@@ -70,6 +70,19 @@ __global__ void __launch_bounds__(384, 1)
   }
   const int n = max(nk[0], nk[1]);
 
+  // column group c of the keys (kPerTile a tile) into its place in the ring
+  auto load_group = [&](int c) {
+    const int j = c / kPerTile, i = c % kPerTile, s = c % kRing;
+    const int row = static_cast<int>(r.k0) + j * BN;
+    unsigned char* dst = sm + Sm::RING + s * kAtom;
+    mbar_arrive_expect_tx(full + s, kAtom);
+    if (i < 2) tma_load_3d(dst, &maps.kn, full + s, 64 * i, h, row);
+    else if (i == 2) tma_load_2d(dst, &maps.kp, full + s, 0, row);
+    else tma_load_3d(dst, &maps.v, full + s, 64 * (i - 3), h, row);
+  };
+  const int first = min(kRing, kPerTile * n);  // groups the ring holds without waiting
+  if (warp == 2 && lane < 4)
+    tma_prefetch_desc(lane == 0 ? &maps.q : lane == 1 ? &maps.kn : lane == 2 ? &maps.kp : &maps.v);
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(full + i, 1);
@@ -88,11 +101,13 @@ __global__ void __launch_bounds__(384, 1)
     fence_mbar_init();
     *bail = 0;
     for (int g = 0; g < 2; ++g) {  // on their way while the CTA sets up
-      if (nk[g] == 0) continue;
-      mbar_arrive_expect_tx(q_full + g, 3 * kAtom);
-      for (int i = 0; i < 3; ++i)
-        tma_load_3d(sm + Sm::Q + (3 * g + i) * kAtom, &maps.q, q_full + g, 64 * i, h,
-                    static_cast<int>(r.q0) + i0 + g * BM);
+      if (nk[g] > 0) {
+        mbar_arrive_expect_tx(q_full + g, 3 * kAtom);
+        for (int i = 0; i < 3; ++i)
+          tma_load_3d(sm + Sm::Q + (3 * g + i) * kAtom, &maps.q, q_full + g, 64 * i, h,
+                      static_cast<int>(r.q0) + i0 + g * BM);
+      }
+      for (int c = 3 * g; c < (g ? first : min(first, 3)); ++c) load_group(c);  // keys, then the rest
     }
   }
   if (warp == 1) {
@@ -109,20 +124,11 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 0) {
       // ---------------------------------------------------------------- loads
       if (elect_one()) {
-        int c = 0;
-        for (int j = 0; j < n && !*bail; ++j) {
-          const int row = static_cast<int>(r.k0) + j * BN;
-#pragma unroll
-          for (int i = 0; i < kPerTile; ++i, ++c) {
-            const int s = c % kRing;
-            if (c >= kRing) wait_for(empty + s, (c / kRing - 1) & 1, bail);
-            if (*bail) break;
-            mbar_arrive_expect_tx(full + s, kAtom);
-            unsigned char* dst = sm + Sm::RING + s * kAtom;
-            if (i < 2) tma_load_3d(dst, &maps.kn, full + s, 64 * i, h, row);
-            else if (i == 2) tma_load_2d(dst, &maps.kp, full + s, 0, row);
-            else tma_load_3d(dst, &maps.v, full + s, 64 * (i - 3), h, row);
-          }
+        int c = first;
+        for (; c < kPerTile * n; ++c) {
+          wait_for(empty + c % kRing, (c / kRing - 1) & 1, bail);
+          if (*bail) break;
+          load_group(c);
         }
         for (int g = 0; g < 2; ++g)
           if (nk[g] > 0) mbar_wait(q_full + g, 0, kDrainCycles);
