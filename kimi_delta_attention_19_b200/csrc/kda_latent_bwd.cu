@@ -115,14 +115,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* bail = reinterpret_cast<volatile int*>(sm + kBail);
   const uint32_t sb = smem_u32(sm);
 
-  // Key blocks first, those with the most queries ahead; then query blocks, likewise. Heads
-  // vary fastest.
-  const int blk = static_cast<int>(blockIdx.x / a.H), h = blockIdx.x % a.H;
-  const bool is_k = blk < k_blocks;
+  // Key blocks first, those with the most queries ahead; then query blocks, likewise (the two
+  // kinds in turn took 8 % longer). Groups of 16 heads: the 4K step 797 us, 815 with all 32.
+  const int all_k = k_blocks * a.H;
+  const bool is_k = blockIdx.x < all_k;
+  int h, blk;
+  if (is_k) place_of(blockIdx.x, a.H, k_blocks, 16, h, blk);
+  else place_of(blockIdx.x - all_k, a.H, q_blocks, 16, h, blk);
   SeqRange r;
   if (!seq_range(a, blockIdx.y, r)) return;
   const int lag = r.lk - r.lq;  // causal: query i sees keys j <= i + lag
-  const int b0 = (is_k ? blk : k_blocks + q_blocks - 1 - blk) * BM;  // first key or query
+  const int b0 = (is_k ? blk : q_blocks - 1 - blk) * BM;  // first key or query
   if (b0 >= (is_k ? r.lk : r.lq)) return;
   if (sb & 1023) {
     if (tid == 0 && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);

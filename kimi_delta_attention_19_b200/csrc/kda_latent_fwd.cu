@@ -49,8 +49,9 @@ __global__ void __launch_bounds__(384, 1)
   volatile int* bail = reinterpret_cast<volatile int*>(sm + Sm::BAIL);
   const uint32_t sb = smem_u32(sm);
 
-  // Heads vary fastest, the blocks with the most keys to see come first.
-  const int h = blockIdx.x % a.H, qb = q_blocks - 1 - static_cast<int>(blockIdx.x / a.H);
+  int h, qb;  // of a head's blocks those with the most keys to see come first
+  place_of(blockIdx.x, a.H, q_blocks, 8, h, qb);
+  qb = q_blocks - 1 - qb;
   SeqRange r;
   if (!seq_range(a, blockIdx.y, r)) return;
   const int i0 = qb * 2 * BM;

@@ -135,6 +135,16 @@ __device__ __forceinline__ void copy_rows(const unsigned char* tile, unsigned ch
   }
 }
 
+// Head and block of place x in the order of a launch: the heads of a group vary fastest, then the
+// blocks, then the groups. The CTAs that run at a time then walk few heads' keys, which stay in
+// the L2, and a group's heavy blocks still come before its light ones (8K x 32-head prompt 604 us
+// with groups of 8, 613 of 16, 605 of 4, 626 with all heads, 638 head by head).
+__device__ __forceinline__ void place_of(int x, int H, int blocks, int group, int& h, int& block) {
+  const int g = x / (group * blocks), in = x % (group * blocks), width = min(group, H - g * group);
+  h = g * group + in % width;
+  block = in / width;
+}
+
 // Tiled bf16 tensor map of `rank` dimensions (the innermost one contiguous, strides in bytes
 // of the others), whose boxes land in the 128-byte-swizzled operand layout.
 bool make_tensor_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
