@@ -206,14 +206,16 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     fence_mbar_init();
     *bail = 0;
     bad_tile[0] = bad_tile[1] = 0;
-    rec->cont = rec->lead = -1;
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.x);
+    griddep_wait();
+    rec->cont = rec->lead = -1;
   }
   if (warp == 1) {
     tmem_alloc(tmem, kCols);
     tmem_relinquish();
   }
+  griddep_wait();  // so far nothing was read or written that a kernel before this one may touch
   // This CTA's run: tiles [t0, t1) of all sequences' tiles in order.
   const int per = (d.N + kThreads - 1) / kThreads;
   int64_t mine = 0;
@@ -738,6 +740,7 @@ __global__ void __launch_bounds__(512, NC == 64 ? 2 : 1) join_kernel(const Args 
   __shared__ float4 acc_s[16][32];
   __shared__ float2 ml_s[16];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  griddep_launch_dependents();  // (a next call sets up meanwhile)
   griddep_wait();
   constexpr bool kPairs = NC <= 32;  // (of 64 rows the unneeded loads cost more: 111 us for 104)
   constexpr int kRows = kJoinRows / 4;  // of a thread
@@ -788,15 +791,16 @@ __global__ void __launch_bounds__(512, NC == 64 ? 2 : 1) join_kernel(const Args 
         const float2 y = lane < np ? ml[at(lane, row)] : make_float2(-INFINITY, 0.f);
         float M, f = 0.f, l = 0.f;
         float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-        for (int p0 = 0; p0 < np; p0 += 4) {
-          float4 v[4][2];
+        constexpr int kAtOnce = 4;
+        for (int p0 = 0; p0 < np; p0 += kAtOnce) {
+          float4 v[kAtOnce][2];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
+          for (int p = 0; p < kAtOnce; ++p) {
             const float* src = part + static_cast<int64_t>(at(min(p0 + p, np - 1), row)) * DC + ch;
             v[p][0] = *reinterpret_cast<const float4*>(src);
             v[p][1] = *reinterpret_cast<const float4*>(src + 128);
           }
-          if (p0 == 0) {  // weights and their sum, while the first four are on their way
+          if (p0 == 0) {  // weights and their sum, while the first are on their way
             M = y.x;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -806,7 +810,7 @@ __global__ void __launch_bounds__(512, NC == 64 ? 2 : 1) join_kernel(const Args 
             for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
           }
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
+          for (int p = 0; p < kAtOnce; ++p) {
             const float fp = __shfl_sync(0xffffffffu, f, (p0 + p) & 31);
             if (p0 + p >= np) continue;
             add(acc[0], fp, v[p][0]);
@@ -883,18 +887,22 @@ cudaError_t launch(const DecodeLatentArgs& d, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  kern<<<grid, Roles<NC, F8>::kThreads, Sm<NC>::BYTES, st>>>(m, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // both may set up while what is before them on the stream finishes
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, NC / kJoinRows);
-  cfg.blockDim = dim3(512);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Roles<NC, F8>::kThreads);
+  cfg.dynamicSmemBytes = Sm<NC>::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, m, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(grid, NC / kJoinRows);
+  cfg.blockDim = dim3(512);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<NC>, a);
 }
 
