@@ -49,6 +49,29 @@ __global__ void __launch_bounds__(384, 1)
   volatile int* bail = reinterpret_cast<volatile int*>(sm + Sm::BAIL);
   const uint32_t sb = smem_u32(sm);
 
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(q_full + g, 1);
+      mbar_init(s_full + g, 1);
+      mbar_init(p_half + g, 128);
+      mbar_init(p_full + g, 128);
+      mbar_init(o_full + g, 1);
+    }
+    mbar_init(drain, 1);
+    mbar_init(v_last, 1);
+    mbar_init(v_fixed, 32);
+    fence_mbar_init();
+    *bail = 0;
+  }
+  if (warp == 2 && lane < 4)
+    tma_prefetch_desc(lane == 0 ? &maps.q : lane == 1 ? &maps.kn : lane == 2 ? &maps.kp : &maps.v);
+  griddep_launch_dependents();
+  griddep_wait();  // so far nothing was read that a kernel before this one may have written
+
   int h, qb;  // of a head's blocks those with the most keys to see come first
   place_of(blockIdx.x, a.H, q_blocks, 8, h, qb);
   qb = q_blocks - 1 - qb;
@@ -82,25 +105,7 @@ __global__ void __launch_bounds__(384, 1)
     else tma_load_3d(dst, &maps.v, full + s, 64 * (i - 3), h, row);
   };
   const int first = min(kRing, kPerTile * n);  // groups the ring holds without waiting
-  if (warp == 2 && lane < 4)
-    tma_prefetch_desc(lane == 0 ? &maps.q : lane == 1 ? &maps.kn : lane == 2 ? &maps.kp : &maps.v);
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
-    }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(q_full + g, 1);
-      mbar_init(s_full + g, 1);
-      mbar_init(p_half + g, 128);
-      mbar_init(p_full + g, 128);
-      mbar_init(o_full + g, 1);
-    }
-    mbar_init(drain, 1);
-    mbar_init(v_last, 1);
-    mbar_init(v_fixed, 32);
-    fence_mbar_init();
-    *bail = 0;
     for (int g = 0; g < 2; ++g) {  // on their way while the CTA sets up
       if (nk[g] > 0) {
         mbar_arrive_expect_tx(q_full + g, 3 * kAtom);
@@ -386,9 +391,17 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.max_q + 2 * BM - 1) / (2 * BM);
   if (blocks * a.H > 0x7fffffff) return cudaErrorInvalidValue;
-  fwd_kernel<<<dim3(static_cast<unsigned>(blocks * a.H), a.n_seqs), 384, Sm::BYTES, st>>>(
-      m, a, static_cast<int>(blocks));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};  // it may set up while what is before it on the stream finishes
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * a.H), a.n_seqs);
+  cfg.blockDim = dim3(384);
+  cfg.dynamicSmemBytes = Sm::BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fwd_kernel, m, a, static_cast<int>(blocks));
 }
 
 }  // namespace latent
