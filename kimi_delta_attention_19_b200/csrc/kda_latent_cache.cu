@@ -15,7 +15,7 @@
 // waited for first, a write and a read of 61 K tokens took 53 us).
 #include <cuda_fp8.h>
 
-#include "kda_latent.cuh"
+#include "kda_latent_tc.cuh"
 
 namespace kda {
 namespace latent {
@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(kWarps * 32)
                        int32_t* status) {
   const int lane = threadIdx.x % 32;
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32) * kTokens;
+  griddep_launch_dependents();
+  griddep_wait();
   if (t0 >= T) return;
   uint4 v[kTokens][2], p[kTokens];
   int64_t slot[kTokens];
@@ -116,6 +118,8 @@ __global__ void __launch_bounds__(kWarps * 32)
                       __nv_bfloat16* out, int32_t* status) {
   const int lane = threadIdx.x % 32;
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32) * kTokens;
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t end = min(T, static_cast<int64_t>(cu[n_seqs]));
   if (t0 >= end) return;
   int lo = 0, hi = n_seqs;  // the last s in [0, n_seqs) with cu[s] <= t0
@@ -195,17 +199,16 @@ cudaError_t launch_cache_write(const __nv_bfloat16* c, int64_t c_token, const __
                                int64_t pe_token, const int64_t* slots, int64_t T,
                                const CacheArgs& cache, int32_t* status, cudaStream_t st) {
   auto kern = cache.format == KDA_CACHE_E4M3 ? cache_write_kernel<true> : cache_write_kernel<false>;
-  kern<<<grid_of(T), kWarps * 32, 0, st>>>(c, c_token, pe, pe_token, slots, T, cache, status);
-  return cudaGetLastError();
+  return launch_early(kern, dim3(grid_of(T)), kWarps * 32, 0, st, c, c_token, pe, pe_token, slots, T,
+                      cache, status);
 }
 
 cudaError_t launch_cache_read(const CacheArgs& cache, const int32_t* table, int64_t table_pages,
                               const int32_t* cu, const int32_t* starts, int n_seqs, int64_t T,
                               __nv_bfloat16* out, int32_t* status, cudaStream_t st) {
   auto kern = cache.format == KDA_CACHE_E4M3 ? cache_read_kernel<true> : cache_read_kernel<false>;
-  kern<<<grid_of(T), kWarps * 32, 0, st>>>(cache, table, table_pages, cu, starts, n_seqs, T, out,
-                                          status);
-  return cudaGetLastError();
+  return launch_early(kern, dim3(grid_of(T)), kWarps * 32, 0, st, cache, table, table_pages, cu, starts,
+                      n_seqs, T, out, status);
 }
 
 }  // namespace latent

@@ -887,23 +887,9 @@ cudaError_t launch(const DecodeLatentArgs& d, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  // both may set up while what is before them on the stream finishes
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(Roles<NC, F8>::kThreads);
-  cfg.dynamicSmemBytes = Sm<NC>::BYTES;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, m, a);
+  e = launch_early(kern, dim3(grid), Roles<NC, F8>::kThreads, Sm<NC>::BYTES, st, m, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(grid, NC / kJoinRows);
-  cfg.blockDim = dim3(512);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<NC>, a);
+  return launch_early(join_kernel<NC>, dim3(grid, NC / kJoinRows), 512, 0, st, a);
 }
 
 }  // namespace

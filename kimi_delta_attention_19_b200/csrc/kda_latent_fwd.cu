@@ -391,17 +391,8 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.max_q + 2 * BM - 1) / (2 * BM);
   if (blocks * a.H > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};  // it may set up while what is before it on the stream finishes
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks * a.H), a.n_seqs);
-  cfg.blockDim = dim3(384);
-  cfg.dynamicSmemBytes = Sm::BYTES;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fwd_kernel, m, a, static_cast<int>(blocks));
+  return launch_early(fwd_kernel, dim3(static_cast<unsigned>(blocks * a.H), a.n_seqs), 384, Sm::BYTES,
+                      st, m, a, static_cast<int>(blocks));
 }
 
 }  // namespace latent

@@ -155,6 +155,25 @@ bool make_tensor_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* 
 bool make_head_map(CUtensorMap* m, const void* ptr, int channels, int64_t heads, int64_t head,
                    int64_t rows, int64_t token, uint32_t box_rows);
 
+// Launches a kernel that may be scheduled while what is before it on the stream finishes (once
+// every CTA there has triggered or ended); it calls griddep_wait() before it reads or writes
+// anything another kernel touches.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                         A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // The device's SM count (148 on B200): the width of the persistent grids.
 int sm_count();
 
