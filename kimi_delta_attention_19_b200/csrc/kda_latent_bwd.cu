@@ -378,33 +378,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       // dV: 64 columns a warpgroup; dK: 96 (the second one's last 64 are k_pe's, fp32). Through
       // shared memory, which nothing else needs any more: whole lines go out.
 #pragma unroll 1
-      for (int q = 0; q < 10; ++q) {
-        uint32_t o[16];
-        const bool is_v = q < 4;
-        const int col = is_v ? 64 * g + 16 * q : 96 * g + 16 * (q - 4), rw = w * 32 + lane;
+      for (int q = 0; q < 5; ++q) {
+        uint32_t o[32];
+        const bool is_v = q < 2;
+        const int col = is_v ? 64 * g + 32 * q : 96 * g + 32 * (q - 2), rw = w * 32 + lane;
         if (n > 0) {
-          tmem_ld16(lanes + (is_v ? DVC : DK) + col, o);
+          tmem_ld32(lanes + (is_v ? DVC : DK) + col, o);
           tmem_ld_wait(o);
         } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = 0;
+          for (int k = 0; k < 32; ++k) o[k] = 0;
         }
         const float mul = is_v ? 1.f : a.scale;
         if (!is_v && col >= DN) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 8; ++k)
             *reinterpret_cast<float4*>(sm + SmK::ST + sw128_chunk(rw, (col - DN) / 4 + k, kAtom)) =
                 make_float4(__uint_as_float(o[4 * k]) * mul, __uint_as_float(o[4 * k + 1]) * mul,
                             __uint_as_float(o[4 * k + 2]) * mul, __uint_as_float(o[4 * k + 3]) * mul);
           continue;
         }
-        uint32_t x[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          x[k] = pack2(__uint_as_float(o[2 * k]) * mul, __uint_as_float(o[2 * k + 1]) * mul);
         unsigned char* tile = sm + (is_v ? SmK::V : SmK::K);
-        *reinterpret_cast<uint4*>(tile + sw128_chunk(rw, col / 8, kAtom)) = make_uint4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<uint4*>(tile + sw128_chunk(rw, col / 8 + 1, kAtom)) = make_uint4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = pack2(__uint_as_float(o[8 * k + 2 * e]) * mul, __uint_as_float(o[8 * k + 2 * e + 1]) * mul);
+          *reinterpret_cast<uint4*>(tile + sw128_chunk(rw, col / 8 + k, kAtom)) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
       }
       group_sync(3, kSoft);
       const int rows = min(BM, r.lk - b0);
