@@ -20,7 +20,7 @@
 // on the host: lengths may change under a captured graph.
 //
 // Warps: 0 loads (TMA boxes of a page's rows, 64 channels wide; two 74 KB stages, each in
-// five groups that are loaded and released separately), 1 issues S^T, 2 O^T, 4-7 softmax and
+// groups of channels that are loaded and released separately), 1 issues S^T, 2 O^T, 4-7 softmax and
 // results (4-11 for 64 rows, 32 a warpgroup); with an 8-bit cache the warps behind them read
 // the codes and write them as bf16 (exact) into the stage.
 #include "kda_latent_tc.cuh"
@@ -33,7 +33,7 @@ constexpr int KT = 64;                    // keys of a tile
 constexpr int kAtoms = DX / 64;           // 64-channel column groups of a tile
 constexpr uint32_t kAtom = KT * 128;      // bytes of one
 constexpr uint32_t kStage = kAtoms * kAtom;
-constexpr int kGroups = 5;                // column groups loaded together: 4 x 128 channels, k_pe
+constexpr int kGroups = 5;                // barriers of a stage, full and empty
 constexpr int kMaxCtas = 160;             // of the workspace; the grid is at most this
 constexpr float kRaise = 8.f;             // log2 units a score may pass its column's reference
 
@@ -163,6 +163,9 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char sm[];
   using S = Sm<NC>;
   using R = Roles<NC, F8>;
+  // Column groups of a tile, loaded and released together: the latent in two (a wait or a commit
+  // costs an issuing thread ~90 clocks) or, as it is converted, in four; then k_pe.
+  constexpr int kG = F8 ? 5 : 3, kGA = F8 ? 2 : 4;  // groups, 64-channel atoms of a latent one
   constexpr int NW = NC / R::kSoft, NH = NW / 2;  // rows of a softmax warpgroup, of a thread
   constexpr uint32_t kCols = NC == 64 ? 512 : NC == 32 ? 256 : 128;  // 4 NC of O^T, 2 NC of S^T
   constexpr int kThreads = R::kThreads;
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < 10; ++i) {
-      mbar_init(full + i, F8 && i % kGroups < 4 ? 8 : 1);
+      mbar_init(full + i, F8 && i % kGroups < kG - 1 ? 8 : 1);
       mbar_init(empty + i, 1);
     }
     mbar_init(s_full, 1);
@@ -310,9 +313,9 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
           const bool any_bad = __any_sync(0xffffffffu, bad);
           const int nb = __popc(__ballot_sync(0xffffffffu, there));
           const int row = static_cast<int>(page * ps + pos % ps);
-          const int y = __shfl_sync(0xffffffffu, row, lane >> 1 & 3);
-  #pragma unroll
-          for (int g = F8 ? 4 : 0; g < kGroups; ++g) {
+          const int y = __shfl_sync(0xffffffffu, row, lane / kGA & 3);
+#pragma unroll
+          for (int g = F8 ? kG - 1 : 0; g < kG; ++g) {
             if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
             stop |= bailed(bail);
             if (stop) continue;
@@ -320,20 +323,20 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
             // (the stage's last tile has been looked at once its O^T is under way)
             if (!F8 && g == 0 && any_bad && lane == 0) bad_tile[s] = t + 1;
             uint64_t* f = full + s * kGroups + g;
-            if (lane == 0) mbar_arrive_expect_tx(f, nb * pr * (g < 4 ? 256 : 128));
+            if (lane == 0) mbar_arrive_expect_tx(f, nb * pr * (g < kG - 1 ? kGA * 128 : 128));
             __syncwarp();
-            const int atom = 2 * g + (lane & 1);
-            if (lane < 2 * nb && atom < kAtoms)
-              tma_load_2d(sm + S::X + s * kStage + atom * kAtom + (lane >> 1) * pr * 128, &maps.x, f,
+            const int atom = kGA * g + lane % kGA;
+            if (lane < kGA * nb && atom < kAtoms)
+              tma_load_2d(sm + S::X + s * kStage + atom * kAtom + lane / kGA * pr * 128, &maps.x, f,
                           F8 ? kPe8 / 2 : atom * 64, y);
           }
           if (seg > 0 && i == 0) load_q();
         }
       }
       if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, kDrainCycles);
-      constexpr int kPer = F8 ? 1 : kGroups;  // groups a tile
+      constexpr int kPer = F8 ? 1 : kG;  // groups a tile
       for (int k = max(0, groups - 2 * kPer); k < groups; ++k)
-        mbar_wait(full + (k / kPer & 1) * kGroups + (F8 ? 4 : k % kPer), k / kPer / 2 & 1, kDrainCycles);
+        mbar_wait(full + (k / kPer & 1) * kGroups + (F8 ? kG - 1 : k % kPer), k / kPer / 2 & 1, kDrainCycles);
     } else if (warp == 1) {
       // --------------------------------------------------------- products: S^T
       // Two warps issue, so that O^T of a tile waits neither for the next tile to arrive nor for
@@ -349,19 +352,19 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
             const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage, 16, 1024);
             const uint64_t qb = sdesc_sw128(sb + S::Q, 16, 1024);
             if (t >= 2) wait_for(s_read + s, (t / 2 - 1) & 1, bail);
-  #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
               wait_for(full + s * kGroups + g, t / 2 & 1, bail);
               tc_fence_after();
-  #pragma unroll
-              for (int k = 0; k < (g < 4 ? 8 : 4); ++k) {
-                const int at = 2 * g + k / 4;  // column group
+#pragma unroll
+              for (int k = 0; k < (g < kG - 1 ? 4 * kGA : 4); ++k) {
+                const int at = kGA * g + k / 4;  // atom
                 umma_bf16(dst, xa + at * (kAtom / 16) + k % 4 * 2, qb + at * (NC * 8) + k % 4 * 2, iq,
                           g > 0 || k > 0);
               }
             }
             umma_commit(s_full + s);
-            umma_commit(empty + s * kGroups + 4);
+            umma_commit(empty + s * kGroups + kG - 1);
             if (i + 1 == wk.cnt) umma_commit(q_empty);
           }
         }
@@ -380,17 +383,16 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
             const int s = t & 1;
             const uint64_t pb = sdesc_sw128(sb + S::P, 8192, 1024);
             const uint64_t xa = sdesc_sw128(sb + S::X + s * kStage, kAtom, 1024);
-            for (int g = 0; g < 4; ++g) wait_for(full + s * kGroups + g, t / 2 & 1, bail);
-            wait_for(p_full, t & 1, bail);
+            wait_for(p_full, t & 1, bail);  // so S^T is formed, and the tile is there
             if (i == 0 && seg > 0) wait_for(o_free, (seg - 1) & 1, bail);
             tc_fence_after();
-  #pragma unroll
+#pragma unroll
             for (int mb = 0; mb < 4; ++mb) {
-  #pragma unroll
+#pragma unroll
               for (int k = 0; k < 4; ++k)
                 umma_bf16(tb + mb * NC, xa + 2 * mb * (kAtom / 16) + 128 * k, pb + 128 * k, ip,
                           i > 0 || k > 0);
-              umma_commit(empty + s * kGroups + mb);
+              if ((2 * mb + 2) % kGA == 0) umma_commit(empty + s * kGroups + 2 * mb / kGA);
             }
             umma_commit(pv_done);
           }
