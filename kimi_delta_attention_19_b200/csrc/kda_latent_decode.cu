@@ -33,7 +33,7 @@ constexpr int KT = 64;                    // keys of a tile
 constexpr int kAtoms = DX / 64;           // 64-channel column groups of a tile
 constexpr uint32_t kAtom = KT * 128;      // bytes of one
 constexpr uint32_t kStage = kAtoms * kAtom;
-constexpr int kGroups = 5;                // barriers of a stage, full and empty
+constexpr int kGroups = 3;                // column groups of a tile: twice 256 channels, k_pe
 constexpr int kMaxCtas = 160;             // of the workspace; the grid is at most this
 constexpr float kRaise = 8.f;             // log2 units a score may pass its column's reference
 
@@ -118,13 +118,14 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 // factor is a bf16 number (`be` = e + 127 <= 134), else two.
 __device__ __forceinline__ void values16(const uint4& code, uint32_t be, uint32_t (&v)[8]) {
   const uint32_t w[4] = {code.x, code.y, code.z, code.w};
-  uint32_t nan = 0;
+  uint32_t most = 0;  // the largest magnitudes, as bits: NaN's is above every value's
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t lo = __byte_perm(w[k], 0, 0x1404), hi = __byte_perm(w[k], 0, 0x3424);
-    v[2 * k] = (lo & 0x80008000u) | (lo >> 4 & 0x07f007f0u);  // codes were in the upper bytes
-    v[2 * k + 1] = (hi & 0x80008000u) | (hi >> 4 & 0x07f007f0u);
-    nan |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
+    const uint32_t ml = lo >> 4 & 0x07f007f0u, mh = hi >> 4 & 0x07f007f0u;  // (from the upper bytes)
+    v[2 * k] = (lo & 0x80008000u) | ml;
+    v[2 * k + 1] = (hi & 0x80008000u) | mh;
+    most = __vimax3_u16x2(most, ml, mh);
   }
   if (be <= 134) {
     const uint32_t f = (be + 120) * 0x00800080u;
@@ -134,7 +135,7 @@ __device__ __forceinline__ void values16(const uint4& code, uint32_t be, uint32_
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = mul2(mul2(v[k], 0x7b807b80u), be * 0x00800080u);
   }
-  if (nan & 0x80808080u) {
+  if ((most + 0x00100010u) & 0x08000800u) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const uint32_t c = w[k / 2] >> (16 * (k & 1));
@@ -144,7 +145,7 @@ __device__ __forceinline__ void values16(const uint4& code, uint32_t be, uint32_
   }
 }
 
-// Softmax warpgroups (up to 32 columns each), sets of eight converting warps, and registers a
+// Softmax warpgroups (up to 32 columns each), converting ones (8-bit caches), and registers a
 // thread: of the first warpgroup, the softmax ones and the converting ones (8-bit caches).
 template <int NC, bool F8>
 struct Roles {
@@ -163,17 +164,17 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char sm[];
   using S = Sm<NC>;
   using R = Roles<NC, F8>;
-  // Column groups of a tile, loaded and released together: the latent in two (a wait or a commit
-  // costs an issuing thread ~90 clocks) or, as it is converted, in four; then k_pe.
-  constexpr int kG = F8 ? 5 : 3, kGA = F8 ? 2 : 4;  // groups, 64-channel atoms of a latent one
+  // Column groups are loaded and released together; few, as a wait or a commit costs an issuing
+  // thread ~90 clocks.
+  constexpr int kG = kGroups, kGA = 4;            // groups, 64-channel atoms of a latent one
   constexpr int NW = NC / R::kSoft, NH = NW / 2;  // rows of a softmax warpgroup, of a thread
   constexpr uint32_t kCols = NC == 64 ? 512 : NC == 32 ? 256 : 128;  // 4 NC of O^T, 2 NC of S^T
   constexpr int kThreads = R::kThreads;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR);
-  uint64_t *full = bar, *empty = bar + 10, *s_full = bar + 20, *p_full = bar + 22,
-           *pv_done = bar + 23, *q_full = bar + 24, *q_empty = bar + 25, *o_free = bar + 26,
-           *s_read = bar + 27, *drain = bar + 29;
+  uint64_t *full = bar, *empty = bar + 6, *s_full = bar + 12, *p_full = bar + 14, *pv_done = bar + 15,
+           *q_full = bar + 16, *q_empty = bar + 17, *o_free = bar + 18, *s_read = bar + 19,
+           *drain = bar + 21;
   uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + S::TM);
   volatile int* bail = reinterpret_cast<volatile int*>(sm + S::BAIL);
   volatile int* bad_tile = reinterpret_cast<volatile int*>(sm + S::BADT);
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < 10; ++i) {
+    for (int i = 0; i < 2 * kGroups; ++i) {
       mbar_init(full + i, F8 && i % kGroups < kG - 1 ? 8 : 1);
       mbar_init(empty + i, 1);
     }
@@ -620,12 +621,10 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
   } else if (F8) {
     // ------------------------------------------- 8-bit rows, as bf16 into the stages
     reg_dec<R::kRc>();
-    // Sets of eight warps; of two, one takes the even 128-channel groups and one the odd ones
-    // (k_pe is copied as it is, by TMA). Four threads a row; of a group one takes the codes
-    // 16 q .. and 64 + 16 q .., so that 8 threads' stores touch all banks. A group's registers
-    // are refilled with the next tile's codes as soon as they are converted; the block table is
-    // read a tile further ahead.
-    constexpr int kSets = R::kSets, kMine = 4 / (kSets > 0 ? kSets : 1);  // groups of a set
+    // Two sets of eight warps, one a column group (k_pe is copied as it is, by TMA). Four threads
+    // a row; of 128 channels (a scale's) one takes the codes 16 q .. and 64 + 16 q .., so that 8
+    // threads' stores touch all banks. The registers are refilled with the next tile's codes as
+    // soon as they are converted; the block table is read a tile further ahead.
     const int i = tid - 128 - 128 * R::kSoft, set = i / 256, row = i % 256 / 4, qd = i % 4;
     Walk ahead = wk;
     int left = n_tiles, in_seg = 0;
@@ -656,10 +655,10 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     auto ld = [&](const unsigned char* p, int off) {
       return p != nullptr ? __ldg(reinterpret_cast<const uint4*>(p + off)) : zero;
     };
-    uint4 code[kMine][2];
-    auto load = [&](const unsigned char* p, int k) {  // group kSets k + set
+    uint4 code[2][2];
+    auto load = [&](const unsigned char* p, int k) {  // 128 channels of the set's 256
 #pragma unroll
-      for (int h = 0; h < 2; ++h) code[k][h] = ld(p, (kSets * k + set) * 128 + h * 64 + qd * 16);
+      for (int h = 0; h < 2; ++h) code[k][h] = ld(p, (2 * set + k) * 128 + h * 64 + qd * 16);
     };
     auto load_ex = [&](const unsigned char* p) {
       return p != nullptr ? __ldg(reinterpret_cast<const uint32_t*>(p + kExp8)) : 0;
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     bool bad = p0 == nullptr && r0.off >= 0;
     Row nxt = fetch();
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) load(p0, k);
+    for (int k = 0; k < 2; ++k) load(p0, k);
     uint32_t ex = load_ex(p0);
     const uint32_t sw = row & 7;
     unsigned char* const row_at = sm + S::X + (row >> 3) * 1024 + sw * 128;
@@ -680,24 +679,26 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
       nxt = fetch();
       unsigned char* const dst = row_at + s * kStage;
 #pragma unroll
-      for (int k = 0; k < kMine; ++k) {
-        const int g = kSets * k + set;
+      for (int k = 0; k < 2; ++k) {
+        const int g = 2 * set + k;  // of 128 channels
         uint32_t v[2][8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) values16(code[k][h], ex >> (8 * g) & 0xffu, v[h]);
         load(np, k);
-        if (t >= 2) wait_for(empty + s * kGroups + g, (t / 2 - 1) & 1, bail);
-        if (k == 0 && bad) bad_tile[s] = t + 1;  // (the stage's last tile has been looked at)
+        if (k == 0) {
+          if (t >= 2) wait_for(empty + s * kGroups + set, (t / 2 - 1) & 1, bail);
+          if (bad) bad_tile[s] = t + 1;  // (the stage's last tile has been looked at)
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             *reinterpret_cast<uint4*>(dst + (2 * g + h) * kAtom + ((qd * 2 + j) ^ sw) * 16) =
                 make_uint4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full + s * kGroups + g);
       }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + s * kGroups + set);
       ex = load_ex(np);
       bad = nbad;
     }

@@ -228,3 +228,23 @@ def test_every_sequence_of_a_full_batch_has_a_bad_page(latent, quantized):
     out = latent.latent_decode(q, cache, table, sl, status=st)
     assert latent.status_of(st) == (4, 3)
     assert torch.isnan(out[bad].float()).all() and torch.equal(out[~bad], good[~bad])
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+def test_a_nan_in_a_cached_row_reaches_its_sequence_only(latent, quantized):
+    """Every one of the 512 channels, each in a sequence of its own: that sequence's rows are NaN
+    in that channel (and in every channel where the score is NaN too, as it is), no other's."""
+    n, ps = 512, 16
+    lens = [20] * n
+    gen = torch.Generator(device=DEV).manual_seed(15)
+    table, pages = paged(lens, ps, seed=15)
+    cache = latent.latent_cache(pages, ps, quantized=quantized, device=DEV)
+    c, pe = rnd(gen, 20 * n, 512), rnd(gen, 20 * n, 64)
+    pick = torch.arange(n, device=DEV)
+    c[20 * pick[::2] + 7, pick[::2]] = math.nan           # every other sequence
+    latent.latent_cache_write(c, pe, cache, slots_of(table, lens, ps))
+    q = rnd(gen, n, 1, 5, 576)
+    out = latent.latent_decode(q, cache, table, torch.full((n,), 20, dtype=torch.int32, device=DEV))
+    assert torch.isnan(out[::2].float()).all() and torch.isfinite(out[1::2].float()).all()
+    want, bnd, _ = ref.absorbed(q[1::2], cache, table[1::2], lens[1::2])
+    ref.inside(out[1::2], want, bnd, "out")
