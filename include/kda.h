@@ -280,8 +280,12 @@ kda_status kda_decode_step(const void *q, const void *k, const void *v, const vo
  *      s_j = scale q . [c_j | k_pe_j],  p = softmax_j(s),  out = sum_j p_j c_j
  *
  * Scores, softmax statistics and sums are fp32; probabilities and score gradients enter
- * the tensor cores as bf16. lse is the natural log of the sum of exponentials. A row that
- * sees no key has out = 0 and lse = -inf (and adds nothing to any gradient).
+ * the tensor cores as bf16 (score gradients of sequences' first rows, where a query sees at
+ * most 128 keys, in two bf16 terms). lse is the natural log of the sum of exponentials. A row
+ * that sees no key has out = 0 and lse = -inf (and adds nothing to any gradient). A key or
+ * value that is not finite may reach any row of its own sequence, masked from it or not, and
+ * never another sequence's; a query that is not finite reaches its own row's results only,
+ * and the gradients of the keys.
  *
  * Every function takes `status`, an int32 device word or NULL, which receives 1 for a
  * malformed or too long sequence, 2 for an expired bounded wait and 3 for a page or slot
@@ -391,7 +395,7 @@ typedef struct {
     int32_t N;          /* sequences */
     int32_t L;          /* query tokens of each (1: plain decode; up to 64 drafted tokens) */
     int32_t H;          /* heads */
-    int64_t table_pages;/* columns of block_table */
+    int64_t table_pages;/* columns of block_table; times page_size below 2^31 - 512 */
     kda_dtype dtype;    /* KDA_BF16 */
     float scale;        /* of the expanded head: 0 selects 1/sqrt(128 + d_pe) */
 } kda_latent_decode_shape;

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     if constexpr (F8) {
       const uint32_t e = exps[i] >> (8 * (lane / 8)) & 0xffu;
-      const float scale = __uint_as_float(e << 23);
+      const float scale = __uint_as_float(max(e << 23, 0x00400000u));  // (2^-127: a subnormal)
       const uint32_t w[4] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w};
       uint32_t r[8];
 #pragma unroll

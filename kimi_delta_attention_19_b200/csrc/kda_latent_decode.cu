@@ -23,6 +23,8 @@
 // groups of channels that are loaded and released separately), 1 issues S^T, 2 O^T, 4-7 softmax and
 // results (4-11 for 64 rows, 32 a warpgroup); with an 8-bit cache the warps behind them read
 // the codes and write them as bf16 (exact) into the stage.
+#include <cuda_fp16.h>
+
 #include "kda_latent_tc.cuh"
 
 namespace kda {
@@ -108,40 +110,23 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// Eight e4m3 codes' words as bf16 pairs times 2^e, exactly. A code's bits in a bf16's place read
-// as its value times 2^-120, so the value is that times 2^(120 + e): one product where the
-// factor is a bf16 number (`be` = e + 127 <= 134), else two.
+// Sixteen e4m3 codes times 2^(be - 127) as bf16 pairs, exactly and with NaN: the conversion to
+// fp16 holds every code, and an fp32 product has the range (2^-127 for be = 0 is a subnormal).
+// Moving a code's bits into a bf16's place takes more integer instructions and a search for
+// NaN codes: 0.263 ms against 0.244 for 256 sequences of up to 8 K.
 __device__ __forceinline__ void values16(const uint4& code, uint32_t be, uint32_t (&v)[8]) {
   const uint32_t w[4] = {code.x, code.y, code.z, code.w};
-  uint32_t most = 0;  // the largest magnitudes, as bits: NaN's is above every value's
+  const float f = __uint_as_float(max(be << 23, 0x00400000u));
+  const float2 ff = make_float2(f, f);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = __byte_perm(w[k], 0, 0x1404), hi = __byte_perm(w[k], 0, 0x3424);
-    const uint32_t ml = lo >> 4 & 0x07f007f0u, mh = hi >> 4 & 0x07f007f0u;  // (from the upper bytes)
-    v[2 * k] = (lo & 0x80008000u) | ml;
-    v[2 * k + 1] = (hi & 0x80008000u) | mh;
-    most = __vimax3_u16x2(most, ml, mh);
-  }
-  if (be <= 134) {
-    const uint32_t f = (be + 120) * 0x00800080u;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], f);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = mul2(mul2(v[k], 0x7b807b80u), be * 0x00800080u);
-  }
-  if ((most + 0x00100010u) & 0x08000800u) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t c = w[k / 2] >> (16 * (k & 1));
-      if ((c & 0x7fu) == 0x7fu) v[k] |= 0x7fffu;
-      if ((c & 0x7f00u) == 0x7f00u) v[k] |= 0x7fff0000u;
-    }
+  for (int k = 0; k < 8; ++k) {
+    uint32_t h;
+    const auto c = static_cast<unsigned short>(w[k / 2] >> (16 * (k & 1)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    __half2 hh;
+    memcpy(&hh, &h, 4);
+    const float2 x = mul2f(__half22float2(hh), ff);
+    v[k] = pack2(x.x, x.y);
   }
 }
 

@@ -248,3 +248,33 @@ def test_a_nan_in_a_cached_row_reaches_its_sequence_only(latent, quantized):
     assert torch.isnan(out[::2].float()).all() and torch.isfinite(out[1::2].float()).all()
     want, bnd, _ = ref.absorbed(q[1::2], cache, table[1::2], lens[1::2])
     ref.inside(out[1::2], want, bnd, "out")
+
+
+def test_every_code_and_scale_of_a_row_in_8_bits(latent):
+    """Rows put together by hand: all codes, scales the cache writes (bytes 7 to 247) and 2^-127 (0),
+    which stands in rows nothing was written to. Read back exactly (a value below bf16's range
+    rounds, one above it is infinite, as a conversion from 64 bits does), and attended to."""
+    n, ps = 48, 16
+    gen = torch.Generator(device=DEV).manual_seed(16)
+    cache = latent.latent_cache(n // ps, ps, quantized=True, device=DEV)
+    flat = cache.view(n, 656)
+    codes = torch.arange(512, device=DEV) % 256
+    flat[:, :512] = torch.stack([codes[torch.randperm(512, generator=gen, device=DEV)]
+                                 for _ in range(n)]).to(torch.uint8)
+    flat[:, 512:640] = rnd(gen, n, 64).view(torch.uint8)
+    exps = torch.tensor([0, 7, 100, 119, 127, 134, 135, 200, 246, 247], device=DEV)
+    flat[:, 640:644] = exps[torch.randint(len(exps), (n, 4), generator=gen, device=DEV)].to(torch.uint8)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV)
+    got = latent.latent_cache_read(cache, table, cu([n]), total=n)
+    at = slots_of(table, [n], ps)
+    torch.testing.assert_close(got, ref.rows_of(cache)[at].to(torch.bfloat16), rtol=0, atol=0,
+                               equal_nan=True)
+
+    flat[:, :512][flat[:, :512] & 127 == 127] = 5          # no NaN, and scores of ordinary size
+    flat[:, 640:644] = exps[torch.randint(5, (n, 4), generator=gen, device=DEV)].to(torch.uint8)
+    q = rnd(gen, 1, 3, 16, 576, std=0.02)
+    lse = torch.empty(1, 3, 16, device=DEV)
+    out = latent.latent_decode(q, cache, table, torch.tensor([n], dtype=torch.int32, device=DEV), lse=lse)
+    want, bnd, want_lse = ref.absorbed(q, cache, table, [n])
+    ref.inside(out, want, bnd, "out")
+    ref.lse_close(lse, want_lse)
