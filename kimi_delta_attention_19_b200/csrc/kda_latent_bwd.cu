@@ -637,6 +637,11 @@ int64_t blocks(int64_t n, int per) { return (n + per - 1) / per; }
 }  // namespace
 
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t st) {
+  // (first: it makes the device's context current in a thread that has none yet, as autograd's,
+  // which the encoding of maps needs)
+  cudaError_t e = cudaFuncSetAttribute(bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kBytes);
+  if (e != cudaSuccess) return e;
   const int64_t tq = a.cu_q != nullptr ? a.Tq : a.Tq * a.n_seqs;
   const int64_t tk = a.cu_k != nullptr ? a.Tk : a.Tk * a.n_seqs;
   Maps m;
@@ -659,9 +664,6 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t st) {
         !make_tensor_map(&m.kps, a.kp, 2, dims, strides, box_s))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kBytes);
-  if (e != cudaSuccess) return e;
   if (tq > 0)
     prepare_kernel<<<dim3(static_cast<unsigned>(blocks(tq, 32)), a.H), 256, 0, st>>>(a, tq);
   const int64_t kb = blocks(a.max_k, BM), qb = blocks(a.max_q, BM);

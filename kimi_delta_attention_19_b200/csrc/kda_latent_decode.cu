@@ -854,6 +854,12 @@ int block_rows(int L, int H) {
 
 template <int NC, bool F8>
 cudaError_t launch(const DecodeLatentArgs& d, cudaStream_t st) {
+  // (first: it makes the device's context current in a thread that has none yet, as autograd's,
+  // which the encoding of maps needs)
+  auto kern = decode_kernel<NC, F8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Sm<NC>::BYTES);
+  if (e != cudaSuccess) return e;
   Args a{d, (d.L * d.H + NC - 1) / NC, d.L * d.H};
   Maps m;
   memset(&m, 0, sizeof m);
@@ -869,10 +875,6 @@ cudaError_t launch(const DecodeLatentArgs& d, cudaStream_t st) {
     const uint32_t box[2] = {64, static_cast<uint32_t>(d.c.page_size < KT ? d.c.page_size : KT)};
     if (!make_tensor_map(&m.x, d.c.cache, 2, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  auto kern = decode_kernel<NC, F8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Sm<NC>::BYTES);
-  if (e != cudaSuccess) return e;
   const int sms = sm_count();
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   e = launch_early(kern, dim3(grid), Roles<NC, F8>::kThreads, Sm<NC>::BYTES, st, m, a);

@@ -372,6 +372,11 @@ __global__ void __launch_bounds__(384, 1)
 }  // namespace
 
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
+  // (first: it makes the device's context current in a thread that has none yet, as autograd's,
+  // which the encoding of maps needs)
+  cudaError_t e = cudaFuncSetAttribute(fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Sm::BYTES);
+  if (e != cudaSuccess) return e;
   const int64_t tq = a.cu_q != nullptr ? a.Tq : a.Tq * a.n_seqs;
   const int64_t tk = a.cu_k != nullptr ? a.Tk : a.Tk * a.n_seqs;
   Maps m;
@@ -386,9 +391,6 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
     const uint32_t box[2] = {64, BN};
     if (!make_tensor_map(&m.kp, a.kp, 2, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Sm::BYTES);
-  if (e != cudaSuccess) return e;
   const int64_t blocks = (a.max_q + 2 * BM - 1) / (2 * BM);
   if (blocks * a.H > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_early(fwd_kernel, dim3(static_cast<unsigned>(blocks * a.H), a.n_seqs), 384, Sm::BYTES,

@@ -4,6 +4,7 @@ streams. Against the fp64 references of tests/latent_ref.py."""
 from __future__ import annotations
 
 import math
+import threading
 
 import pytest
 import torch
@@ -278,3 +279,52 @@ def test_every_code_and_scale_of_a_row_in_8_bits(latent):
     want, bnd, want_lse = ref.absorbed(q, cache, table, [n])
     ref.inside(out, want, bnd, "out")
     ref.lse_close(lse, want_lse)
+
+
+def test_threads_without_a_context(latent):
+    """Each call as the first that a thread makes to the GPU (autograd's threads start like that)."""
+    q, kn, pe, v, g = expanded_inputs([150], [150], 2, seed=18)
+    dec = decode_case(latent, [150, 9], 5, 1, 16, False, seed=18)
+    cache, table = dec[1], dec[2]
+    off, slots = cu([9, 9]), torch.arange(18, device=DEV)
+    c, c_pe = q[:18, 0].repeat(1, 3)[:, :512].contiguous(), pe[:18]
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+
+    def results():
+        n = dec[0].shape[:3]
+        return {"out": torch.empty(150, 2, 128, dtype=torch.bfloat16, device=DEV),
+                "lse": torch.empty(150, 2, device=DEV),
+                "grads": tuple(torch.empty(t.shape, dtype=t.dtype, device=DEV) for t in (q, kn, pe, v)),
+                "decode": torch.empty(*n, 512, dtype=torch.bfloat16, device=DEV),
+                "cache": torch.zeros_like(cache),
+                "read": torch.empty(18, 576, dtype=torch.bfloat16, device=DEV)}
+
+    def calls(r):
+        return (lambda: latent.latent_attn_fwd(q, kn, pe, v, out=r["out"], lse=r["lse"]),
+                lambda: latent.latent_attn_bwd(q, kn, pe, v, r["out"], r["lse"], g,
+                                               grads=r["grads"], workspace=ws),
+                lambda: latent.latent_decode(*dec, out=r["decode"], workspace=dws),
+                lambda: latent.latent_cache_write(c, c_pe, r["cache"], slots),
+                lambda: latent.latent_cache_read(cache, table, off, out=r["read"]))
+
+    dws = latent.latent_decode_workspace(2, 5, cache)
+    want, got, failed = results(), results(), []
+    for call in calls(want):
+        call()
+    torch.cuda.synchronize()
+
+    def run(call):
+        try:
+            call()
+        except Exception as e:
+            failed.append(e)
+
+    for call in calls(got):
+        t = threading.Thread(target=run, args=(call,))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for k in want:
+        for a, b in zip(want[k] if k == "grads" else (want[k],), got[k] if k == "grads" else (got[k],)):
+            assert torch.equal(a, b), k
