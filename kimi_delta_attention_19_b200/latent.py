@@ -316,12 +316,29 @@ class _LatentAttention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, d_out):
-        q, k_nope, k_pe, v, out, lse, cu_q, cu_k = ctx.saved_tensors
-        grads = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device)
-                      for t in (q, k_nope, k_pe, v)) if cu_q is not None else None
-        return latent_attn_bwd(q, k_nope, k_pe, v, out, lse, d_out.contiguous(),
-                               cu_seqlens=cu_q, cu_seqlens_k=cu_k, grads=grads,
-                               **ctx.opts) + (None, None, None)
+        saved = ctx.saved_tensors
+        grads = _Gradients.apply(d_out, *saved, ctx.opts) if torch.is_grad_enabled() \
+            else _gradients(d_out, *saved, ctx.opts)
+        return grads + (None, None, None)
+
+
+def _gradients(d_out, q, k_nope, k_pe, v, out, lse, cu_q, cu_k, opts):
+    grads = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device)
+                  for t in (q, k_nope, k_pe, v)) if cu_q is not None else None
+    return latent_attn_bwd(q, k_nope, k_pe, v, out, lse, d_out.contiguous(), cu_seqlens=cu_q,
+                           cu_seqlens_k=cu_k, grads=grads, **opts)
+
+
+class _Gradients(torch.autograd.Function):
+    """_gradients under create_graph=True: a later pass through them raises, where it would
+    otherwise take them for constants."""
+    @staticmethod
+    def forward(ctx, *args):
+        return _gradients(*args)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("latent_attention offers no gradients of its gradients")
 
 
 def latent_attention(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
@@ -330,8 +347,8 @@ def latent_attention(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, 
                      max_seqlen_k: int = 0, causal: bool = True,
                      scale: float | None = None) -> torch.Tensor:
     """Differentiable expanded latent attention: out as latent_attn_fwd returns it, with
-    gradients for q, k_nope, k_pe and v. Packed rows behind the last sequence come out as
-    zeros, in out and in the gradients."""
+    gradients for q, k_nope, k_pe and v (gradients of gradients are refused). Packed rows
+    behind the last sequence come out as zeros, in out and in the gradients."""
     if cu_seqlens is not None and cu_seqlens_k is None:
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
     return _LatentAttention.apply(q, k_nope, k_pe, v, cu_seqlens, cu_seqlens_k,

@@ -281,6 +281,17 @@ def test_every_code_and_scale_of_a_row_in_8_bits(latent):
     ref.lse_close(lse, want_lse)
 
 
+def test_gradients_of_gradients_are_refused(latent):
+    q, kn, pe, v, g = expanded_inputs([9], [9], 2, seed=17)
+    leaves = [t.detach().clone().requires_grad_() for t in (q, kn, pe, v)]
+    out = latent.latent_attention(*leaves)
+    grads = torch.autograd.grad(out, leaves, g, create_graph=True)
+    plain = torch.autograd.grad(latent.latent_attention(*leaves), leaves, g)
+    assert all(torch.equal(a, b) for a, b in zip(grads, plain))
+    with pytest.raises(RuntimeError, match="no gradients of its gradients"):
+        (out.float().sum() + sum(t.float().square().sum() for t in grads)).backward()
+
+
 def test_threads_without_a_context(latent):
     """Each call as the first that a thread makes to the GPU (autograd's threads start like that)."""
     q, kn, pe, v, g = expanded_inputs([150], [150], 2, seed=18)
