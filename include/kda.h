@@ -281,7 +281,7 @@ kda_status kda_decode_step(const void *q, const void *k, const void *v, const vo
  *
  * Scores, softmax statistics and sums are fp32; probabilities and score gradients enter
  * the tensor cores as bf16 (score gradients of sequences' first rows, where a query sees at
- * most 128 keys, in two bf16 terms). lse is the natural log of the sum of exponentials. A row
+ * most 384 keys, in two bf16 terms). lse is the natural log of the sum of exponentials. A row
  * that sees no key has out = 0 and lse = -inf (and adds nothing to any gradient). A key or
  * value that is not finite may reach any row of its own sequence, masked from it or not, and
  * never another sequence's; a query that is not finite reaches its own row's results only,

@@ -20,8 +20,14 @@
 //
 // dS enters its products as bf16. Rows that see few keys carry most of a gradient's squares and
 // feel the rounding of out in D the most, so steps whose queries see at most kFew keys add what
-// dS lost, as a second bf16 term (relative error of dq and dk on packed documents of 156 to
-// 1432 tokens against 64 bits: 2.5e-3 without, of which 1.7e-3 is the result's own rounding).
+// dS lost, as a second bf16 term. Relative errors of dq against 64 bits (1.66e-3 are the result's
+// own rounding), and the time of packed documents of 156 to 1432 tokens:
+//   kFew                          128      256      384
+//   208 queries of 245 tokens     2.48e-3  1.84e-3  1.84e-3
+//   125 queries of 425 tokens     2.45e-3  2.45e-3  1.77e-3
+//   8 documents of 540 to 655     2.32e-3  2.18e-3  2.09e-3
+//   backward and forward          260 us   263      265
+// From some 400 keys on a row's single term stays below 2.4e-3.
 //
 // In both, S of the next step is issued as soon as this step's is in registers, dP likewise,
 // so the products run beside the exponentials.
@@ -34,7 +40,7 @@ namespace {
 constexpr int BM = 128;                    // queries of a dQ CTA, keys of a dK CTA
 constexpr int BQ = 64;                     // query step of a dK CTA, key step of a dQ CTA
 constexpr uint32_t kAtom = BM * 128, kAtomQ = BQ * 128;
-constexpr int kFew = 128;                  // keys up to which dS is kept in two terms
+constexpr int kFew = 384;                  // keys up to which dS is kept in two terms
 constexpr int kQStages = 3, kKStages = 4, kVStages = 3;
 constexpr int kThreads = 384, kSoft = 256;
 
