@@ -60,6 +60,17 @@ struct Maps {
   CUtensorMap q, qs, dout, douts, kn, kns, kp, kps, v, vs;  // s: boxes of BQ rows
 };
 
+__device__ __forceinline__ float dot8(const __nv_bfloat16* x, const __nv_bfloat16* y) {
+  const uint4 a = *reinterpret_cast<const uint4*>(x), b = *reinterpret_cast<const uint4*>(y);
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    s += __uint_as_float(u[e] << 16) * __uint_as_float(v[e] << 16) +
+         __uint_as_float(u[e] & 0xffff0000u) * __uint_as_float(v[e] & 0xffff0000u);
+  return s;
+}
+
 // (lse log2 e, D) of 32 tokens of a head a block; a row without keys gets +inf: p = 0. Half a
 // warp a row (16 bytes a lane of dO and of out), all of a warp's loads at once.
 __global__ void __launch_bounds__(256) prepare_kernel(AttnArgs a, int64_t tq) {
@@ -91,6 +102,41 @@ __global__ void __launch_bounds__(256) prepare_kernel(AttnArgs a, int64_t tq) {
   __syncthreads();
   if (threadIdx.x < 32 && t0 + threadIdx.x < tq)
     a.stat[h * tq + t0 + threadIdx.x] = st[threadIdx.x];
+}
+
+// D of the queries that see at most 32 keys, a warp a query and a lane a key: sum_j p_j (dO . v_j).
+// The rounding of out, from which other rows' D comes, is a large part of the little that their
+// dS holds (dq of sequences of 1 to 3 tokens was off by 5.5e-3, and is by 1.7e-3). In a launch of
+// its own: found by prepare_kernel's warps these rows cost 40 us of a packed step, here 15.
+__global__ void __launch_bounds__(256) few_kernel(AttnArgs a, int64_t tq) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.z;
+  SeqRange r;
+  if (!seq_range(a, blockIdx.y, r)) return;
+  const int lag = r.lk - r.lq;  // causal: query i sees i + 1 + lag keys
+  const int first = a.causal ? max(0, -lag) : 0;
+  const int last = a.causal ? (lag < 32 ? min(r.lq, 32 - lag) : 0) : r.lk <= 32 ? r.lq : 0;
+  for (int64_t i = first + static_cast<int64_t>(blockIdx.x) * 8 + warp; i < last; i += 8 * gridDim.x) {
+    const int see = a.causal ? static_cast<int>(i) + 1 + lag : r.lk;
+    const int64_t t = r.q0 + i;
+    float2* st = a.stat + h * tq + t;
+    float s = 0.f, dp = 0.f;
+    if (lane < see) {
+      const int64_t j = r.k0 + lane;
+      const __nv_bfloat16 *q = a.q + t * a.qt + h * a.qh, *g = a.dout + (t * a.H + h) * DV;
+      const __nv_bfloat16 *kn = a.kn + j * a.kt + h * a.kh, *kp = a.kp + j * a.pt,
+                          *v = a.v + j * a.vt + h * a.vh;
+#pragma unroll
+      for (int c = 0; c < DN; c += 8) s += dot8(q + c, kn + c);
+#pragma unroll
+      for (int c = 0; c < DP; c += 8) s += dot8(q + DN + c, kp + c);
+#pragma unroll
+      for (int c = 0; c < DV; c += 8) dp += dot8(g + c, v + c);
+      dp *= ex2(fmaf(s, a.scale * kLog2e, -st->x));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dp += __shfl_xor_sync(0xffffffffu, dp, off);
+    if (lane == 0) st->y = dp;
+  }
 }
 
 // what the bf16 pair `hi` of (x, y) lost, as another pair
@@ -670,8 +716,10 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t st) {
         !make_tensor_map(&m.kps, a.kp, 2, dims, strides, box_s))
       return cudaErrorInvalidValue;
   }
-  if (tq > 0)
+  if (tq > 0) {
     prepare_kernel<<<dim3(static_cast<unsigned>(blocks(tq, 32)), a.H), 256, 0, st>>>(a, tq);
+    few_kernel<<<dim3(4, a.n_seqs, a.H), 256, 0, st>>>(a, tq);
+  }
   const int64_t kb = blocks(a.max_k, BM), qb = blocks(a.max_q, BM);
   if ((kb + qb) * a.H > 0x7fffffff) return cudaErrorInvalidValue;
   bwd_kernel<<<dim3(static_cast<unsigned>((kb + qb) * a.H), a.n_seqs), kThreads, kBytes, st>>>(

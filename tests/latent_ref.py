@@ -22,7 +22,7 @@ def bound(result, sum_abs, tiny=1e-6):
 def expanded(q, k_nope, k_pe, v, lq, lk, causal, scale=None, d_out=None, out_used=None):
     """Packed references: out, lse, bounds and (with d_out) gradients and their bounds, as a
     dict; a dict's "b_x" bounds "x". Rows of no sequence are NaN. out_used: the out the
-    backward was given (its D is formed from it)."""
+    backward was given (D of rows that see more than 32 keys is formed from it)."""
     scale = scale if scale is not None else 1 / math.sqrt(q.shape[-1])
     H = q.shape[1]
     r = {}
@@ -60,7 +60,10 @@ def expanded(q, k_nope, k_pe, v, lq, lk, causal, scale=None, d_out=None, out_use
             continue
         g = d_out[sq].double().transpose(0, 1)
         oo = out_used[sq].double().transpose(0, 1)
-        ds = scale * p * (g @ V.transpose(1, 2) - (g * oo).sum(-1, keepdim=True))
+        dp = g @ V.transpose(1, 2)
+        few = (x > -math.inf).sum(-1, keepdim=True) <= 32   # there D is the formula's own sum
+        D = torch.where(few, (p * dp).sum(-1, keepdim=True), (g * oo).sum(-1, keepdim=True))
+        ds = scale * p * (dp - D)
         # fp32 sums inside dP and D (128 terms at 2^-24 of their magnitudes) before the
         # difference, the exponential, and ds rounded to bf16
         slack = scale * p * ((g.abs() @ V.abs().transpose(1, 2))

@@ -339,3 +339,43 @@ def test_threads_without_a_context(latent):
     for k in want:
         for a, b in zip(want[k] if k == "grads" else (want[k],), got[k] if k == "grads" else (got[k],)):
             assert torch.equal(a, b), k
+
+
+@pytest.mark.parametrize("lq,lk,causal", [([1, 2, 3, 0, 5, 32], [1, 2, 3, 7, 5, 32], True),
+                                          ([28], [28], True), ([9, 40], [20, 12], True),
+                                          ([70, 3], [30, 1], False), ([1] * 100, [2] * 100, True)])
+def test_gradients_of_short_sequences(latent, lq, lk, causal):
+    """Rows of up to 32 keys: dS as exact as fp32 scores make it (two bf16 terms keep 2^-16 of it,
+    dP and D are fp32 sums of 128 products), whatever out was rounded to."""
+    q, kn, pe, v, g = expanded_inputs(lq, lk, 3, seed=19)
+    kw = dict(cu_seqlens=cu(lq), cu_seqlens_k=cu(lk), max_seqlen=max(lq), max_seqlen_k=max(lk),
+              causal=causal)
+    out, lse = latent.latent_attn_fwd(q, kn, pe, v, **kw)
+    dq, dkn, dpe, _ = latent.latent_attn_bwd(q, kn, pe, v, out, lse, g, **kw)
+    a0 = b0 = 0
+    for a, b in zip(lq, lk):
+        sq, sk = slice(a0, a0 + a), slice(b0, b0 + b)
+        a0, b0 = a0 + a, b0 + b
+        Q, G, V = (t.double().transpose(0, 1) for t in (q[sq], g[sq], v[sk]))
+        K = torch.cat((kn[sk].double(), pe[sk].double()[:, None].expand(-1, 3, -1)), -1).transpose(0, 1)
+        x = Q @ K.transpose(1, 2) / math.sqrt(192)
+        seen = torch.ones(a, b, dtype=torch.bool, device=DEV)
+        if causal:
+            seen = torch.arange(b, device=DEV)[None] <= torch.arange(a, device=DEV)[:, None] + b - a
+        x = x.masked_fill(~seen, -math.inf)
+        p = torch.nan_to_num(torch.softmax(x, -1))
+        dp = G @ V.transpose(1, 2)
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True)) / math.sqrt(192)
+        # p off by 2^-17 (scores of 192 products, the exponential), dP and D by as much of the
+        # magnitudes they are summed from
+        size = G.abs() @ V.abs().transpose(1, 2)
+        e = 2.0 ** -15 * ds.abs() + \
+            2.0 ** -16 * p * (size + (p * size).sum(-1, keepdim=True)) / math.sqrt(192)
+
+        def check(got, val, err, name):
+            ref.inside(got, val, 1.05 * ref.U * val.abs() + err + 1e-6, name)
+
+        check(dq[sq].transpose(0, 1), ds @ K, e @ K.abs(), "dq")
+        dk, ek = ds.transpose(1, 2) @ Q, e.transpose(1, 2) @ Q.abs()
+        check(dkn[sk].transpose(0, 1), dk[..., :128], ek[..., :128], "dk_nope")
+        check(dpe[sk], dk[..., 128:].sum(0), ek[..., 128:].sum(0), "dk_pe")
