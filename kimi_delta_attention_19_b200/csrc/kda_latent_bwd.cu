@@ -26,7 +26,7 @@
 //   208 queries of 245 tokens     2.48e-3  1.84e-3  1.84e-3
 //   125 queries of 425 tokens     2.45e-3  2.45e-3  1.77e-3
 //   8 documents of 540 to 655     2.32e-3  2.18e-3  2.09e-3
-//   backward and forward          260 us   263      265
+//   backward and forward          260 us   263      265      (before few_kernel)
 // From some 400 keys on a row's single term stays below 2.4e-3.
 //
 // In both, S of the next step is issued as soon as this step's is in registers, dP likewise,
@@ -60,8 +60,10 @@ struct Maps {
   CUtensorMap q, qs, dout, douts, kn, kns, kp, kps, v, vs;  // s: boxes of BQ rows
 };
 
-__device__ __forceinline__ float dot8(const __nv_bfloat16* x, const __nv_bfloat16* y) {
-  const uint4 a = *reinterpret_cast<const uint4*>(x), b = *reinterpret_cast<const uint4*>(y);
+__device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
   float s = 0.f;
 #pragma unroll
@@ -104,38 +106,45 @@ __global__ void __launch_bounds__(256) prepare_kernel(AttnArgs a, int64_t tq) {
     a.stat[h * tq + t0 + threadIdx.x] = st[threadIdx.x];
 }
 
-// D of the queries that see at most 32 keys, a warp a query and a lane a key: sum_j p_j (dO . v_j).
+// D of the queries that see at most 32 keys, a warp a query: sum_j p_j (dO . v_j).
 // The rounding of out, from which other rows' D comes, is a large part of the little that their
 // dS holds (dq of sequences of 1 to 3 tokens was off by 5.5e-3, and is by 1.7e-3). In a launch of
-// its own: found by prepare_kernel's warps these rows cost 40 us of a packed step, here 15.
+// its own: found by prepare_kernel's warps these rows cost 40 us of a packed step, here 9 (a lane a key: 15).
 __global__ void __launch_bounds__(256) few_kernel(AttnArgs a, int64_t tq) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.z;
   SeqRange r;
   if (!seq_range(a, blockIdx.y, r)) return;
   const int lag = r.lk - r.lq;  // causal: query i sees i + 1 + lag keys
   const int first = a.causal ? max(0, -lag) : 0;
-  const int last = a.causal ? (lag < 32 ? min(r.lq, 32 - lag) : 0) : r.lk <= 32 ? r.lq : 0;
+  const int last = a.causal ? static_cast<int>(min(static_cast<int64_t>(r.lq), int64_t{32} - lag)) : r.lk <= 32 ? r.lq : 0;
   for (int64_t i = first + static_cast<int64_t>(blockIdx.x) * 8 + warp; i < last; i += 8 * gridDim.x) {
     const int see = a.causal ? static_cast<int>(i) + 1 + lag : r.lk;
     const int64_t t = r.q0 + i;
     float2* st = a.stat + h * tq + t;
-    float s = 0.f, dp = 0.f;
-    if (lane < see) {
-      const int64_t j = r.k0 + lane;
-      const __nv_bfloat16 *q = a.q + t * a.qt + h * a.qh, *g = a.dout + (t * a.H + h) * DV;
-      const __nv_bfloat16 *kn = a.kn + j * a.kt + h * a.kh, *kp = a.kp + j * a.pt,
-                          *v = a.v + j * a.vt + h * a.vh;
+    const int c = 8 * (lane % 8);  // eight lanes a key: whole lines
+    const __nv_bfloat16 *q = a.q + t * a.qt + h * a.qh + c, *g = a.dout + (t * a.H + h) * DV + c;
+    const uint4 q0 = ld16(q), q1 = ld16(q + 64), q2 = ld16(q + DN), g0 = ld16(g), g1 = ld16(g + 64);
+    const float lse2 = st->x;
+    float sum = 0.f;
 #pragma unroll
-      for (int c = 0; c < DN; c += 8) s += dot8(q + c, kn + c);
+    for (int k = 0; k < 32; k += 4) {
+      float s = 0.f, dp = 0.f;
+      if (k + lane / 8 < see) {
+        const int64_t j = r.k0 + k + lane / 8;
+        const __nv_bfloat16 *kn = a.kn + j * a.kt + h * a.kh + c, *v = a.v + j * a.vt + h * a.vh + c;
+        s = dot8(q0, ld16(kn)) + dot8(q1, ld16(kn + 64)) + dot8(q2, ld16(a.kp + j * a.pt + c));
+        dp = dot8(g0, ld16(v)) + dot8(g1, ld16(v + 64));
+      }
 #pragma unroll
-      for (int c = 0; c < DP; c += 8) s += dot8(q + DN + c, kp + c);
-#pragma unroll
-      for (int c = 0; c < DV; c += 8) dp += dot8(g + c, v + c);
-      dp *= ex2(fmaf(s, a.scale * kLog2e, -st->x));
+      for (int off = 4; off > 0; off >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, off);
+        dp += __shfl_xor_sync(0xffffffffu, dp, off);
+      }
+      if (k + lane / 8 < see) sum += dp * ex2(fmaf(s, a.scale * kLog2e, -lse2));
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) dp += __shfl_xor_sync(0xffffffffu, dp, off);
-    if (lane == 0) st->y = dp;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (lane == 0) st->y = sum;
   }
 }
 
