@@ -41,14 +41,23 @@ def _compile(src: str, obj: str, extra: list[str] | None = None) -> str:
     return r.stderr  # ptxas -v report
 
 
-# Test-only variant of the library: the first wait on the inputs in each tensor-core prefill
+# Test-only variants of the library. In one the first wait on the inputs in each tensor-core prefill
 # kernel, and any wait in a latent-attention kernel, gives up after 64 clocks, so a test can
 # watch the kernels' bail-out path (status word set, copies and products drained, tensor memory
-# freed) run on the GPU and the context stay usable. The product never loads it.
+# freed) run on the GPU and the context stay usable. The product never loads them.
 SHORTWAIT_LIB = os.path.join(PKG, "libkda_shortwait.so")
 SHORTWAIT_DEFINES = {"kda_prefill_tc.cu": ["-DKDA_FIRST_WAIT_LIMIT=64", "-DKDA_FIRST_WAIT_STUCK=1"],
                      **{f"kda_latent_{k}.cu": ["-DKDA_LATENT_WAIT_CYCLES=64"]
                         for k in ("fwd", "bwd", "decode")}}
+
+# A second one, whose latent-attention kernels give up the wait for a unit's last products, when
+# every other role is done or about to be.
+LASTWAIT_LIB = os.path.join(PKG, "libkda_lastwait.so")
+LASTWAIT_DEFINES = {f"kda_latent_{k}.cu": ["-DKDA_LATENT_RESULTS_GIVEN_UP"]
+                    for k in ("fwd", "bwd", "decode")}
+
+VARIANTS = {"shortwait": (SHORTWAIT_LIB, SHORTWAIT_DEFINES),
+            "lastwait": (LASTWAIT_LIB, LASTWAIT_DEFINES)}
 
 
 def _link(lib: str, objs: list[str]) -> None:
@@ -89,20 +98,20 @@ def build(verbose: bool = False) -> str:
     deps = sources + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
         [os.path.join(ROOT, "include", "kda.h")]
     newest_dep = max(os.path.getmtime(p) for p in deps)
-    objs, short_objs = [], []
+    objs, of_variant = [], {name: [] for name in VARIANTS}
     jobs = {}
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(sources) + len(SHORTWAIT_DEFINES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, 2 * len(sources))) as ex:
         for src in sources:
             name = os.path.basename(src)
             obj = os.path.join(BUILD, name + ".o")
             objs.append(obj)
             todo = [(obj, [])]
-            if name in SHORTWAIT_DEFINES:
-                sobj = os.path.join(BUILD, name + ".shortwait.o")
-                short_objs.append(sobj)
-                todo.append((sobj, SHORTWAIT_DEFINES[name]))
-            else:
-                short_objs.append(obj)
+            for variant, (_, defines) in VARIANTS.items():
+                vobj = obj
+                if name in defines:
+                    vobj = os.path.join(BUILD, f"{name}.{variant}.o")
+                    todo.append((vobj, defines[name]))
+                of_variant[variant].append(vobj)
             for o, extra in todo:
                 if os.path.exists(o) and os.path.getmtime(o) >= newest_dep:
                     continue
@@ -116,7 +125,8 @@ def build(verbose: bool = False) -> str:
             if verbose:
                 print(f"== {jobs[fut][0]} {' '.join(jobs[fut][1])}\n{report}", file=sys.stderr)
     _link(LIB, objs)
-    _link(SHORTWAIT_LIB, short_objs)
+    for variant, (path, _) in VARIANTS.items():
+        _link(path, of_variant[variant])
     return LIB
 
 

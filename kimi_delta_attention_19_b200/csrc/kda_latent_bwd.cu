@@ -354,10 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(empty + t % kQStages);
         }
         umma_commit(o_full);
-        if (*bail) {
-          umma_commit(drain);
-          mbar_wait(drain, 0, kDrainCycles);
-        }
+        umma_commit(drain);
+        mbar_wait(drain, 0, kDrainCycles);
       }
     } else if (warp == 2 && n > 0 && r.lq - (j1 - 1) * BQ < BQ) {
       // queries past the sequence may hold anything (0 x NaN is NaN): cleared
@@ -434,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(ds_ready);
       }
-      if (n > 0) wait_for(o_full, 0, bail);
+      if (n > 0) wait_for_results(o_full, 0, bail);
       tc_fence_after();
       // dV: 64 columns a warpgroup; dK: 96 (the second one's last 64 are k_pe's, fp32). Through
       // shared memory, which nothing else needs any more: whole lines go out.
@@ -550,10 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(empty + t % kKStages);
         }
         umma_commit(o_full);
-        if (*bail) {
-          umma_commit(drain);
-          mbar_wait(drain, 0, kDrainCycles);
-        }
+        umma_commit(drain);
+        mbar_wait(drain, 0, kDrainCycles);
       }
     } else if (warp == 2 && n > 0 && r.lk - (n - 1) * BQ < BQ) {
       // keys past the sequence may hold anything (0 x NaN is NaN): cleared once S is formed
@@ -637,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(ds_ready);
       }
-      if (n > 0) wait_for(o_full, 0, bail);
+      if (n > 0) wait_for_results(o_full, 0, bail);
       tc_fence_after();
 #pragma unroll 1
       for (int q = 0; q < 6; ++q) {  // through shared memory: whole lines go out

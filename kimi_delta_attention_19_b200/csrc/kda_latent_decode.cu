@@ -354,10 +354,8 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
             if (i + 1 == wk.cnt) umma_commit(q_empty);
           }
         }
-        if (*bail) {
-          umma_commit(drain);
-          mbar_wait(drain, 0, kDrainCycles);
-        }
+        umma_commit(drain);
+        mbar_wait(drain, 0, kDrainCycles);
       }
     } else if (warp == 2) {
       // --------------------------------------------------------- products: O^T
@@ -383,10 +381,8 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
             umma_commit(pv_done);
           }
         }
-        if (*bail) {
-          umma_commit(drain + 1);
-          mbar_wait(drain + 1, 0, kDrainCycles);
-        }
+        umma_commit(drain + 1);
+        mbar_wait(drain + 1, 0, kDrainCycles);
       }
     }
   } else if (warp < 4 + 4 * R::kSoft) {
@@ -571,7 +567,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
         }
       }
       group_sync(1 + wg, 128);
-      wait_for(pv_done, (t - 1) & 1, bail);
+      wait_for_results(pv_done, (t - 1) & 1, bail);
       tc_fence_after();
 #pragma unroll 1
       for (int q = 0; q < 4 * NW / 16; ++q) {

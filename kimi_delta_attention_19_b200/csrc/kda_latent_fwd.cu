@@ -206,10 +206,8 @@ __global__ void __launch_bounds__(384, 1)
             if (j + 1 < nk[g]) qk(g, j + 1, g == 1 || j + 1 >= nk[1]);
           }
         }
-        if (*bail) {
-          umma_commit(drain);
-          mbar_wait(drain, 0, kDrainCycles);
-        }
+        umma_commit(drain);
+        mbar_wait(drain, 0, kDrainCycles);
       }
     } else if (warp == 2 && n > 0 && r.lk - (n - 1) * BN < BN) {
       // v's rows past the sequence may hold anything (0 x NaN is NaN): cleared
@@ -324,7 +322,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_arrive(p_full + g);
     }
     const float l = l2.x + l2.y;
-    if (nt > 0) wait_for(o_full + g, 0, bail);
+    if (nt > 0) wait_for_results(o_full + g, 0, bail);
     tc_fence_after();
     const float mul = l == 0.f ? 0.f : 1.f / l;
     const bool mine = i < r.lq;

@@ -37,9 +37,11 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 
 // Bounded waits. `bail` is a shared word of the CTA: the first wait that runs out (about a
 // second) sets it, every later wait returns at once, no further copy is issued, and all loops
-// run to their ends (so no named barrier is left short); the CTA then waits (again with a limit)
-// for its products in flight, reports kDevWaitTimeout and frees its tensor memory. The loading
-// thread always waits for its last copies before it is done, whatever became of the others.
+// run to their ends (so no named barrier is left short); the CTA then reports kDevWaitTimeout and
+// frees its tensor memory. The loading thread always waits (again with a limit) for its last
+// copies before it is done, and each issuing thread for its last products, whatever became of
+// the others: a wait that runs out after an issuing thread has looked at `bail` must not free
+// tensor memory that a product still writes.
 #ifndef KDA_LATENT_WAIT_CYCLES  // (the test-only library gives up almost at once)
 #define KDA_LATENT_WAIT_CYCLES 2000000000LL
 #endif
@@ -54,6 +56,16 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatil
       return;
     }
   }
+}
+
+// The wait for a unit's last products, behind which results are read. (A test-only library gives
+// it up at once: the latest that a wait can run out.)
+__device__ __forceinline__ void wait_for_results(uint64_t* bar, uint32_t parity, volatile int* bail) {
+#ifdef KDA_LATENT_RESULTS_GIVEN_UP
+  *bail = 1;
+#else
+  wait_for(bar, parity, bail);
+#endif
 }
 
 __device__ __forceinline__ bool bailed(volatile int* bail) {  // the same answer for a whole warp
