@@ -197,14 +197,15 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     bad_tile[0] = bad_tile[1] = 0;
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.x);
-    griddep_wait();
-    rec->cont = rec->lead = -1;
   }
+  griddep_wait();  // so far nothing was read or written that a kernel before this one may touch
+  if (tid == 0) rec->cont = rec->lead = -1;
+  // (not before: a CTA of the kernel ahead may still need the columns, and would wait for this one
+  // while this one waits for it)
   if (warp == 1) {
     tmem_alloc(tmem, kCols);
     tmem_relinquish();
   }
-  griddep_wait();  // so far nothing was read or written that a kernel before this one may touch
   // This CTA's run: tiles [t0, t1) of all sequences' tiles in order.
   const int per = (d.N + kThreads - 1) / kThreads;
   int64_t mine = 0;
