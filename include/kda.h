@@ -287,10 +287,11 @@ kda_status kda_decode_step(const void *q, const void *k, const void *v, const vo
  * never another sequence's; a query that is not finite reaches its own row's results only,
  * and the gradients of the keys.
  *
- * Every function takes `status`, an int32 device word or NULL, which receives 1 for a
- * malformed or too long sequence, 2 for an expired bounded wait and 3 for a page or slot
- * out of range; it is never cleared (zero it before the calls it should cover;
- * kda_workspace_status(status, 4, ...) reads it). Nothing is allocated and nothing is kept
+ * Every function takes `status`, an int32 device word, which receives 1 for a malformed or
+ * too long sequence, 2 for an expired bounded wait and 3 for a page or slot out of range; it
+ * is never cleared (zero it before the calls it should cover; kda_workspace_status(status, 4,
+ * ...) reads it). Calls given NULL report in a word that the library keeps for the device,
+ * which kda_latent_status reads and clears. Nothing is allocated, and nothing else is kept
  * between calls; every call may be captured in a CUDA graph. Results do not depend on the
  * order in which thread blocks run.
  */
@@ -425,6 +426,15 @@ kda_status kda_latent_decode(const void *q, const void *cache, const int32_t *bl
                              float *lse, const kda_latent_decode_shape *shape,
                              const kda_latent_cache *cache_shape, void *workspace,
                              size_t workspace_bytes, int32_t *status, kda_stream_t stream);
+
+/*
+ * What kda_latent_* calls on the current device without a status word of their own have
+ * reported since this was last called: KDA_OK, or KDA_ERR_DEVICE with a code in
+ * *device_code (may be NULL). Runs behind the work on `stream` and synchronises it, so calls
+ * on other streams are covered once those are done. Not for a stream that is being captured
+ * (a captured call reports at each replay). Diagnostic only.
+ */
+kda_status kda_latent_status(kda_stream_t stream, int32_t *device_code);
 
 /*
  * Synchronises `stream` and reads the device-side status word a previous

@@ -18,6 +18,31 @@ constexpr int kPe8 = DC, kExp8 = DC + 2 * DP;  // byte offsets of k_pe and the e
 constexpr int kMaxDraft = 64;
 constexpr int32_t kDevBadPage = kDevBadSlot;
 
+// Where calls without a status word of their own report: a word of the source file on the device
+// (one each, as a file's kernels cannot name another's variables, and a call need not look an
+// address up), and what take_status read there last.
+[[maybe_unused]] static __device__ int32_t g_word, g_taken;
+
+__device__ __forceinline__ void report(int32_t* status, int32_t code) {
+  atomicExch(status != nullptr ? status : &g_word, code);
+}
+
+[[maybe_unused]] static __global__ void take_kernel() { g_taken = atomicExch(&g_word, kDevOk); }
+
+// Reads and clears this file's word on the current device, behind the work on `st`, which it
+// synchronises. One call at a time (g_taken).
+[[maybe_unused]] static cudaError_t take_status(cudaStream_t st, int32_t* code) {
+  take_kernel<<<1, 1, 0, st>>>();
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(code, g_taken, sizeof *code, 0, cudaMemcpyDeviceToHost, st);
+  return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+cudaError_t take_fwd_status(cudaStream_t st, int32_t* code);
+cudaError_t take_bwd_status(cudaStream_t st, int32_t* code);
+cudaError_t take_decode_status(cudaStream_t st, int32_t* code);
+cudaError_t take_cache_status(cudaStream_t st, int32_t* code);
+
 // Expanded form, resolved on the host.
 struct AttnArgs {
   const __nv_bfloat16 *q, *kn, *kp, *v;
@@ -44,7 +69,7 @@ struct SeqRange {
   int lq, lk;
 };
 
-// False when the sequence is malformed or longer than its bound (status set): skip it.
+// False when the sequence is malformed or longer than its bound (reported): skip it.
 __device__ __forceinline__ bool seq_range(const AttnArgs& a, int s, SeqRange& r) {
   if (a.cu_q == nullptr) {
     r.q0 = s * a.Tq;
@@ -57,7 +82,7 @@ __device__ __forceinline__ bool seq_range(const AttnArgs& a, int s, SeqRange& r)
   const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.Tq && k0 >= 0 && k1 >= k0 && k1 <= a.Tk &&
                   (s != 0 || (q0 == 0 && k0 == 0)) && q1 - q0 <= a.max_q && k1 - k0 <= a.max_k;
   if (!ok) {
-    if (a.status != nullptr) atomicExch(a.status, kDevBadSeqlens);
+    report(a.status, kDevBadSeqlens);
     return false;
   }
   r.q0 = q0;

@@ -1,5 +1,7 @@
 // kda_latent_api.cu -- the latent-attention part of the C ABI (include/kda.h): argument
 // checks, workspace layout and dispatch. Nothing here allocates or synchronises.
+#include <mutex>
+
 #include "kda_latent.cuh"
 
 namespace kda {
@@ -264,6 +266,19 @@ kda_status kda_latent_decode(const void* q, const void* cache, const int32_t* bl
   a.ws = static_cast<unsigned char*>(workspace);
   a.status = status;
   return of(launch_latent_decode(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_latent_status(kda_stream_t stream, int32_t* device_code) {
+  static std::mutex one_at_a_time;
+  std::lock_guard<std::mutex> lock(one_at_a_time);
+  int32_t code = kda::kDevOk;
+  for (auto take : {take_fwd_status, take_bwd_status, take_decode_status, take_cache_status}) {
+    int32_t c = kda::kDevOk;
+    if (take(reinterpret_cast<cudaStream_t>(stream), &c) != cudaSuccess) return KDA_ERR_CUDA;
+    if (c != kda::kDevOk) code = c;
+  }
+  if (device_code != nullptr) *device_code = code;
+  return code == kda::kDevOk ? KDA_OK : KDA_ERR_DEVICE;
 }
 
 }  // extern "C"

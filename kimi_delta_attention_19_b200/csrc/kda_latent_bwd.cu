@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b0 = (is_k ? blk : q_blocks - 1 - blk) * BM;  // first key or query
   if (b0 >= (is_k ? r.lk : r.lq)) return;
   if (sb & 1023) {
-    if (tid == 0 && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
+    if (tid == 0) report(a.status, kDevWaitTimeout);
     return;
   }
   // steps [j0, j1) of queries (dK CTA) or keys (dQ CTA)
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *bail && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
+  if (tid == 0 && *bail) report(a.status, kDevWaitTimeout);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, 512);
@@ -734,6 +734,8 @@ cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t st) {
                  st>>>(a, tk);
   return cudaGetLastError();
 }
+
+cudaError_t take_bwd_status(cudaStream_t st, int32_t* code) { return take_status(st, code); }
 
 }  // namespace latent
 }  // namespace kda

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int i = 0; i < kTokens; ++i) {
     if (slot[i] < 0) continue;
     if (slot[i] >= cache.n_pages * cache.page_size) {
-      if (lane == 0 && status != nullptr) atomicExch(status, kDevBadPage);
+      if (lane == 0) report(status, kDevBadPage);
       continue;
     }
     unsigned char* row = const_cast<unsigned char*>(cache.cache) + slot[i] * (F8 ? kRow8 : DX * 2);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (slot[i] == -1) continue;
     uint4* dst = reinterpret_cast<uint4*>(out + (t0 + i) * DX);
     if (slot[i] == -2) {
-      if (lane == 0 && status != nullptr) atomicExch(status, kDevBadPage);
+      if (lane == 0) report(status, kDevBadPage);
       const uint4 nan = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
       dst[lane] = nan;
       dst[lane + 32] = nan;
@@ -210,6 +210,8 @@ cudaError_t launch_cache_read(const CacheArgs& cache, const int32_t* table, int6
   return launch_early(kern, dim3(grid_of(T)), kWarps * 32, 0, st, cache, table, table_pages, cu, starts,
                       n_seqs, T, out, status);
 }
+
+cudaError_t take_cache_status(cudaStream_t st, int32_t* code) { return take_status(st, code); }
 
 }  // namespace latent
 }  // namespace kda

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
   const Layout wl = ws_layout(NC);
 
   if (sb & 1023) {  // the operand tiles need it, and nothing else is in shared memory
-    if (tid == 0 && d.status != nullptr) atomicExch(d.status, kDevWaitTimeout);
+    if (tid == 0) report(d.status, kDevWaitTimeout);
     return;
   }
   if (tid == 0) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
     const int64_t len = d.lens[n];
     if (tiles_of(d, len) > 0) continue;
     const bool bad = !len_ok(d, len);
-    if (bad && tid == 0 && d.status != nullptr) atomicExch(d.status, kDevBadPage);
+    if (bad && tid == 0) report(d.status, kDevBadPage);
     const uint4 v = bad ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu)
                         : make_uint4(0, 0, 0, 0);
     uint4* o = reinterpret_cast<uint4*>(d.out + static_cast<int64_t>(n) * a.R * DC);
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
       group_sync(1 + wg, 128);
       if (tw < NW) fac[cw] = mul;
       if (tid == 128) {
-        if (bad && d.status != nullptr) atomicExch(d.status, kDevBadPage);
+        if (bad) report(d.status, kDevBadPage);
         const int64_t u0 = gt - wk.st, u1 = u0 + wk.tiles - 1;  // the unit's first, last tile
         const int unit = wk.sn * a.rb + wk.srb;
         const int last_cta = static_cast<int>(((u1 + 1) * G - 1) / total);
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(Roles<NC, F8>::kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *bail && d.status != nullptr) atomicExch(d.status, kDevWaitTimeout);
+  if (tid == 0 && *bail) report(d.status, kDevWaitTimeout);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, kCols);
@@ -910,6 +910,8 @@ cudaError_t launch_latent_decode(const DecodeLatentArgs& d, cudaStream_t st) {
     default: return f8 ? launch<64, true>(d, st) : launch<64, false>(d, st);
   }
 }
+
+cudaError_t take_decode_status(cudaStream_t st, int32_t* code) { return take_status(st, code); }
 
 }  // namespace latent
 }  // namespace kda

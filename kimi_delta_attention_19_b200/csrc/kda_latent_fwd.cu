@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(384, 1)
   const int i0 = qb * 2 * BM;
   if (i0 >= r.lq) return;
   if (sb & 1023) {
-    if (tid == 0 && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
+    if (tid == 0) report(a.status, kDevWaitTimeout);
     return;
   }
   const int lag = r.lk - r.lq;  // causal: query i sees keys j <= i + lag
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *bail && a.status != nullptr) atomicExch(a.status, kDevWaitTimeout);
+  if (tid == 0 && *bail) report(a.status, kDevWaitTimeout);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, 512);
@@ -394,6 +394,8 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t st) {
   return launch_early(fwd_kernel, dim3(static_cast<unsigned>(blocks * a.H), a.n_seqs), 384, Sm::BYTES,
                       st, m, a, static_cast<int>(blocks));
 }
+
+cudaError_t take_fwd_status(cudaStream_t st, int32_t* code) { return take_status(st, code); }
 
 }  // namespace latent
 }  // namespace kda

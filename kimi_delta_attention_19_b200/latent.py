@@ -9,6 +9,7 @@ A token keeps one latent vector c (512) and a shared key part k_pe (64) for all 
                                 of each sequence
     latent_cache                a paged cache, bf16 or with the latent in 8 bits
     latent_cache_write / _read  tokens into the cache and back
+    latent_status               what calls without a `status` tensor have reported
 
 Argument marshalling only: the computation runs in libkda.so's kernels, on the tensors'
 device and on `stream` (default: that device's current stream).
@@ -21,7 +22,7 @@ import ctypes
 import torch
 
 from . import kda
-from .kda import KDA_BF16, KDA_ERR_INVALID_ARG, KDA_OK, KdaError, lib
+from .kda import KDA_BF16, KDA_ERR_DEVICE, KDA_ERR_INVALID_ARG, KDA_OK, KdaError, lib
 
 D_NOPE, D_PE, D_V, D_C = 128, 64, 128, 512
 CACHE_BF16, CACHE_E4M3 = 0, 1
@@ -63,7 +64,8 @@ def _declare(L: ctypes.CDLL) -> None:
     L.kda_latent_decode_workspace_size.argtypes = [dec, cache]
     L.kda_latent_decode_workspace_size.restype = sz
     L.kda_latent_decode.argtypes = [p] * 7 + [dec, cache, p, sz, p, p]
-    for name in ("attn_fwd", "attn_bwd", "cache_write", "cache_read", "decode"):
+    L.kda_latent_status.argtypes = [p, ctypes.POINTER(i32)]
+    for name in ("attn_fwd", "attn_bwd", "cache_write", "cache_read", "decode", "status"):
         getattr(L, "kda_latent_" + name).restype = ctypes.c_int
 
 
@@ -71,7 +73,7 @@ _declare(lib)
 
 EXPORTED = ("kda_latent_attn_fwd", "kda_latent_attn_bwd_workspace_size", "kda_latent_attn_bwd",
             "kda_latent_cache_write", "kda_latent_cache_read",
-            "kda_latent_decode_workspace_size", "kda_latent_decode")
+            "kda_latent_decode_workspace_size", "kda_latent_decode", "kda_latent_status")
 
 
 # The checks of a call are plain conditions (messages are formed only when one fails), pointers
@@ -211,7 +213,9 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v
     tokens of their sequence.
 
     Returns (out [T, H, 128], lse [T, H] fp32, natural log). Rows that see no key have
-    out = 0, lse = -inf; packed rows behind the last sequence are not written.
+    out = 0, lse = -inf; packed rows behind the last sequence are not written. Neither are those
+    of a sequence that is malformed or longer than its bound: `status` (int32 device tensor)
+    receives 1, or without it what latent_status() tells.
     """
     if cu_seqlens is not None and cu_seqlens_k is None:
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
@@ -344,16 +348,19 @@ class _Gradients(torch.autograd.Function):
 def latent_attention(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
                      *, cu_seqlens: torch.Tensor | None = None,
                      cu_seqlens_k: torch.Tensor | None = None, max_seqlen: int = 0,
-                     max_seqlen_k: int = 0, causal: bool = True,
-                     scale: float | None = None) -> torch.Tensor:
+                     max_seqlen_k: int = 0, causal: bool = True, scale: float | None = None,
+                     status: torch.Tensor | None = None) -> torch.Tensor:
     """Differentiable expanded latent attention: out as latent_attn_fwd returns it, with
     gradients for q, k_nope, k_pe and v (gradients of gradients are refused). Packed rows
-    behind the last sequence come out as zeros, in out and in the gradients."""
+    behind the last sequence come out as zeros, in out and in the gradients, and so do those
+    of a sequence that is skipped because cu_seqlens is malformed there or max_seqlen too
+    small: reported as 1 in `status` (int32 device tensor), by the forward and the backward
+    pass, or without one to latent_status()."""
     if cu_seqlens is not None and cu_seqlens_k is None:
         cu_seqlens_k, max_seqlen_k = cu_seqlens, max_seqlen_k or max_seqlen
     return _LatentAttention.apply(q, k_nope, k_pe, v, cu_seqlens, cu_seqlens_k,
                                   dict(max_seqlen=max_seqlen, max_seqlen_k=max_seqlen_k,
-                                       causal=causal, scale=scale))
+                                       causal=causal, scale=scale, status=status))
 
 
 # -------------------------------------------------------------------------------- cache
@@ -530,3 +537,18 @@ def latent_decode_workspace(N: int, H: int, cache: torch.Tensor, *, L: int = 1) 
 
 
 status_of = kda.workspace_status   # (status, device code) of a status word
+
+
+def latent_status(device=None, stream=None) -> tuple[int, int]:
+    """(status, device code) of the calls on `device` (default: the current one) that were given
+    no `status` tensor, since this was last asked: KDA_ERR_DEVICE and 1 for a malformed or too
+    long sequence (left as it was, or zeros from latent_attention), 2 for an expired bounded
+    wait, 3 for a page or slot out of range. Synchronises `stream` (default: the device's
+    current one); calls on other streams are covered once those are done."""
+    code = ctypes.c_int32(0)
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream() if stream is None else stream
+        rc = lib.kda_latent_status(s.cuda_stream, ctypes.byref(code))
+    if rc not in (KDA_OK, KDA_ERR_DEVICE):
+        raise KdaError(rc, "kda_latent_status")
+    return rc, code.value
