@@ -15,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -68,7 +69,8 @@ def _link(lib: str, objs: list[str]) -> None:
 
 
 # The latent-attention binding's extension module (csrc/latent_host.cpp), for this interpreter
-# and this torch.
+# and this torch. Without it (no Python.h, no torch headers, another g++) the library is whole and
+# the binding's calls take some 10 us longer, so that it cannot be built is a warning.
 HOST_MODULE = os.path.join(PKG, "_latent_host.so")
 
 
@@ -117,9 +119,12 @@ def build(verbose: bool = False) -> str:
                     continue
                 jobs[ex.submit(_compile, src, o, extra)] = (name, extra)
         host_src = os.path.join(CSRC, "latent_host.cpp")
+        host = None
         if not os.path.exists(HOST_MODULE) or os.path.getmtime(HOST_MODULE) < max(
                 os.path.getmtime(host_src), os.path.getmtime(os.path.join(ROOT, "include", "kda.h"))):
-            jobs[ex.submit(_build_host, host_src)] = ("latent_host.cpp", [])
+            if os.path.exists(HOST_MODULE):  # (not left behind for another kda.h, should this fail)
+                os.unlink(HOST_MODULE)
+            host = ex.submit(_build_host, host_src)
         for fut in cf.as_completed(jobs):
             report = fut.result()
             if verbose:
@@ -127,6 +132,12 @@ def build(verbose: bool = False) -> str:
     _link(LIB, objs)
     for variant, (path, _) in VARIANTS.items():
         _link(path, of_variant[variant])
+    try:
+        if host is not None and (report := host.result()) and verbose:
+            print(f"== latent_host.cpp\n{report}", file=sys.stderr)
+    except Exception as e:
+        warnings.warn(f"the latent binding's extension module was not built, its calls go the "
+                      f"slower way through latent.py: {e}")
     return LIB
 
 
