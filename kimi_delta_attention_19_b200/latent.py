@@ -329,7 +329,10 @@ class _LatentAttention(torch.autograd.Function):
 def _gradients(d_out, q, k_nope, k_pe, v, out, lse, cu_q, cu_k, opts):
     grads = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device)
                   for t in (q, k_nope, k_pe, v)) if cu_q is not None else None
-    return latent_attn_bwd(q, k_nope, k_pe, v, out, lse, d_out.contiguous(), cu_seqlens=cu_q,
+    d_out = d_out.contiguous()
+    if d_out.data_ptr() % 16:     # a part of a larger gradient, which autograd hands on as a view
+        d_out = d_out.clone()
+    return latent_attn_bwd(q, k_nope, k_pe, v, out, lse, d_out, cu_seqlens=cu_q,
                            cu_seqlens_k=cu_k, grads=grads, **opts)
 
 
