@@ -70,7 +70,9 @@ float scale_of(PyObject* o) {
   if (o == Py_None) return 0.f;
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Unusual{};
-  return static_cast<float>(v);
+  const float f = static_cast<float>(v);
+  if (!(f > 0.f && f <= 3.4028235e38f)) throw Unusual{};  // (0 would select the default)
+  return f;
 }
 
 void* ptr(const at::Tensor& t) { return t.data_ptr(); }

@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 
 import torch
 
@@ -137,6 +138,16 @@ def _addr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _scale(scale: float | None) -> float:
+    """The library's scale, where 0 selects the default: None, and no number, stands for that."""
+    if scale is None:
+        return 0.0
+    s = ctypes.c_float(scale).value
+    if not 0.0 < s < math.inf:
+        raise ValueError(f"scale must be positive and finite in fp32 ({scale})")
+    return s
+
+
 def _check(rc: int, what: str) -> None:
     if rc != KDA_OK:
         raise KdaError(rc, what)
@@ -195,7 +206,7 @@ def _attn_shape(q, k_nope, k_pe, v, cu_q, cu_k, max_q, max_k, causal, scale, ind
     pt, _ = _strides(k_pe, "k_pe", batched)
     return LatentShape(qs[0] if batched else 1, H, qs[-3], Tk, n_seqs, int(max_q), int(max_k),
                        ks[-1], ps[-1], vs[-1], qt, qh, kt, kh, pt, vt, vh, int(bool(causal)),
-                       KDA_BF16, 0.0 if scale is None else float(scale))
+                       KDA_BF16, _scale(scale))
 
 
 def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
@@ -209,7 +220,7 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v
     the heads. Packed sequences come with cu_seqlens (int32 [n + 1]) and, where the keys'
     lengths differ (a cached prefix before the queries), cu_seqlens_k; max_seqlen and
     max_seqlen_k bound the lengths (0: the packed totals; a tight bound makes the launch
-    smaller). causal: query i sees keys up to its own position, the queries being the last
+    smaller). scale: None is 1/sqrt(192). causal: query i sees keys up to its own position, the queries being the last
     tokens of their sequence.
 
     Returns (out [T, H, 128], lse [T, H] fp32, natural log). Rows that see no key have
@@ -477,7 +488,8 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     block_table int32 [N, pages]; seq_lens int32 [N] counts the cached tokens, the query
     tokens included (write them first). Query i sees the cache up to its own token; with
     draft_mask (int64 [N, L]) it sees all before the L last tokens and, of those, token j
-    where bit j of draft_mask[n, i] is set.
+    where bit j of draft_mask[n, i] is set. scale: None is that of the expanded head,
+    1/sqrt(192).
 
     Returns out like q with 512 channels (the value projection is the caller's); `lse`
     (fp32, q's leading shape) receives the natural log-sum-exp. A row that sees nothing has
@@ -507,7 +519,7 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     table_p = _typed(block_table, torch.int32, None, "block_table", at)
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError(f"block_table must be [{N}, pages] (got {tuple(block_table.shape)})")
-    s = DecodeShape(N, L, H, block_table.shape[1], KDA_BF16, 0.0 if scale is None else float(scale))
+    s = DecodeShape(N, L, H, block_table.shape[1], KDA_BF16, _scale(scale))
     if out is None:
         out = q.new_empty(lead + (D_C,))
     else:

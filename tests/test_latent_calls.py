@@ -2,6 +2,8 @@
 for another call than the one made."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -29,3 +31,38 @@ def test_gradient_at_any_address(latent, packed):
     out, lse = latent.latent_attn_fwd(q, kn, pe, v, **kw)
     want = latent.latent_attn_bwd(q, kn, pe, v, out, lse, g, **kw)
     assert all(torch.equal(t.grad, w) for t, w in zip(ins, want))
+
+
+def inputs(H=2, T=8):
+    bf = torch.bfloat16
+    return (torch.zeros(T, H, 192, dtype=bf), torch.zeros(T, H, 128, dtype=bf),
+            torch.zeros(T, 64, dtype=bf), torch.zeros(T, H, 128, dtype=bf))
+
+
+NO_SCALES = [0.0, 0, -0.0, 1e-60, -1.0, math.nan, math.inf, 1e60]
+
+
+@pytest.mark.parametrize("scale", NO_SCALES)
+def test_a_scale_of_zero_is_not_the_default(latent, scale):
+    """The library's 0 selects 1/sqrt(192); a caller's 0 does not mean that, nor what becomes 0 in
+    32 bits."""
+    with pytest.raises(ValueError, match="scale"):
+        latent._attn_shape(*inputs(), None, None, 0, 0, True, scale, -1)
+    with pytest.raises(ValueError, match="scale"):
+        latent._scale(scale)
+    assert latent._scale(None) == 0.0 and latent._scale(0.125) == 0.125
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", NO_SCALES)
+def test_a_scale_of_zero_is_refused_by_every_call(latent, scale):
+    from tests.test_latent_gpu import decode_case
+    x = [t.to(DEV) for t in inputs()]
+    dec = decode_case(latent, [40, 9], 4, 1, 16, False, seed=2)
+    out, lse = latent.latent_attn_fwd(*x)
+    for call in (lambda: latent.latent_attn_fwd(*x, scale=scale),
+                 lambda: latent.latent_attn_bwd(*x, out, lse, out, scale=scale),
+                 lambda: latent.latent_attention(*x, scale=scale),
+                 lambda: latent.latent_decode(*dec, scale=scale)):
+        with pytest.raises(ValueError, match="scale"):
+            call()
