@@ -121,6 +121,8 @@ def _elsewhere(index: int, stream) -> bool:
     """Whether a call on GPU `index` and `stream` has to make them current first."""
     if index < 0:
         raise ValueError("latent attention needs CUDA tensors")
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream is one of {stream.device}, the tensors are on cuda:{index}")
     return stream is not None or torch.cuda.current_device() != index
 
 

@@ -3,6 +3,7 @@ for another call than the one made."""
 from __future__ import annotations
 
 import math
+import types
 
 import pytest
 import torch
@@ -66,3 +67,12 @@ def test_a_scale_of_zero_is_refused_by_every_call(latent, scale):
                  lambda: latent.latent_decode(*dec, scale=scale)):
         with pytest.raises(ValueError, match="scale"):
             call()
+
+
+def test_a_stream_of_another_device_is_refused(latent):
+    """Making it current makes its device current; the call then went to the tensors' device's
+    current stream instead, unordered with what the caller had put on the given one."""
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1))
+    assert latent._elsewhere(1, stream)
+    with pytest.raises(ValueError, match="stream"):
+        latent._elsewhere(0, stream)
