@@ -165,6 +165,8 @@ def _strides(t: torch.Tensor, name: str, batched: bool):
     if st[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}'s channels must be contiguous")
     token = st[-3] if head else st[-2]
+    if batched and shape[1] == 1:    # one token of each sequence: they lie as the sequences do
+        token = st[0]
     if batched and shape[0] != 1 and st[0] != token * shape[1] and t.numel() != 0:
         raise ValueError(f"{name}'s sequences must follow each other (strides {st})")
     # of a dimension of one the stride says nothing

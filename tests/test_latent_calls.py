@@ -76,3 +76,34 @@ def test_a_stream_of_another_device_is_refused(latent):
     assert latent._elsewhere(1, stream)
     with pytest.raises(ValueError, match="stream"):
         latent._elsewhere(0, stream)
+
+
+def last_tokens(B=3, T=5, H=2):
+    """The last token of each sequence of a batch, its queries cut from longer ones."""
+    q, kn, pe, v = (t.unsqueeze(0).repeat(B, *[1] * t.dim()) for t in inputs(H, T))
+    return q[:, -1:], kn, pe, v
+
+
+def test_one_token_of_each_sequence_of_a_batch(latent):
+    """Of a dimension of one the stride says nothing, so the sequences' own stride is the tokens'."""
+    q, kn, pe, v = last_tokens()
+    s = latent._attn_shape(q, kn, pe, v, None, None, 0, 0, True, None, -1)
+    assert (s.B, s.Tq, s.Tk, s.q_token, s.q_head, s.k_token) == (3, 1, 5, 5 * 2 * 192, 192, 2 * 128)
+    s = latent._attn_shape(q, kn[:, :1], pe[:, :1], v[:, :1], None, None, 0, 0, True, None, -1)
+    assert (s.k_token, s.pe_token, s.v_token) == (5 * 2 * 128, 5 * 64, 5 * 2 * 128)
+    s = latent._attn_shape(q[:1], kn[:1], pe[:1], v[:1], None, None, 0, 0, True, None, -1)
+    assert s.B == 1 and s.q_token >= 192 and s.q_token % 8 == 0
+
+
+@pytest.mark.gpu
+def test_one_token_of_each_sequence_of_a_batch_on_the_gpu(latent):
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    x = [torch.randn(t.shape, generator=gen, device=DEV).to(torch.bfloat16) for t in
+         last_tokens(4, 150)]
+    q = torch.randn(4, 9, 2, 192, generator=gen, device=DEV).to(torch.bfloat16)[:, -1:]
+    got, near = latent.latent_attn_fwd(q, *x[1:]), latent.latent_attn_fwd(q.contiguous(), *x[1:])
+    assert all(torch.equal(a, b) for a, b in zip(got, near))
+    g = torch.ones_like(got[0])
+    a = latent.latent_attn_bwd(q, *x[1:], *got, g)
+    b = latent.latent_attn_bwd(q.contiguous(), *x[1:], *got, g)
+    assert all(torch.equal(y, z) for y, z in zip(a, b))
