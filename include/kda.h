@@ -282,10 +282,11 @@ kda_status kda_decode_step(const void *q, const void *k, const void *v, const vo
  * Scores, softmax statistics and sums are fp32; probabilities and score gradients enter
  * the tensor cores as bf16 (score gradients of sequences' first rows, where a query sees at
  * most 384 keys, in two bf16 terms). lse is the natural log of the sum of exponentials. A row
- * that sees no key has out = 0 and lse = -inf (and adds nothing to any gradient). A key or
- * value that is not finite may reach any row of its own sequence, masked from it or not, and
- * never another sequence's; a query that is not finite reaches its own row's results only,
- * and the gradients of the keys.
+ * that sees no key has out = 0, lse = -inf and dq = 0 and adds nothing to any gradient,
+ * whatever its q and d_out hold. A key or value that is not finite may reach any row of its own
+ * sequence, masked from it or not, and never another sequence's; any other query or d_out that
+ * is not finite reaches its own row's results only, and the gradients of its sequence's keys
+ * and values.
  *
  * Every function takes `status`, an int32 device word, which receives 1 for a malformed or
  * too long sequence, 2 for an expired bounded wait and 3 for a page or slot out of range; it

@@ -73,8 +73,9 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return s;
 }
 
-// (lse log2 e, D) of 32 tokens of a head a block; a row without keys gets +inf: p = 0. Half a
-// warp a row (16 bytes a lane of dO and of out), all of a warp's loads at once.
+// (lse log2 e, D) of 32 tokens of a head a block; a row without keys gets +inf (p = 0) and 0 (its
+// dO may hold anything). Half a warp a row (16 bytes a lane of dO and of out), all of a warp's
+// loads at once.
 __global__ void __launch_bounds__(256) prepare_kernel(AttnArgs a, int64_t tq) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.y;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 32;
@@ -99,7 +100,8 @@ __global__ void __launch_bounds__(256) prepare_kernel(AttnArgs a, int64_t tq) {
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (lane % 16 == 0)
-      st[warp * 4 + 2 * k + lane / 16] = make_float2(l[k] == -INFINITY ? INFINITY : l[k] * kLog2e, s);
+      st[warp * 4 + 2 * k + lane / 16] =
+          l[k] == -INFINITY ? make_float2(INFINITY, 0.f) : make_float2(l[k] * kLog2e, s);
   }
   __syncthreads();
   if (threadIdx.x < 32 && t0 + threadIdx.x < tq)
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
            *res_full = bar + 14, *s_full = bar + 15, *dp_full = bar + 16, *s_read = bar + 17,
            *p_ready = bar + 18, *ds_ready = bar + 19, *p_free = bar + 20, *ds_free = bar + 21,
            *o_full = bar + 22, *drain = bar + 23, *last = bar + 24, *fixed = bar + 25,
-           *a_ready = bar + 26;
+           *a_ready = bar + 26, *first = bar + 27, *first_fixed = bar + 28;
   uint32_t* tmem = reinterpret_cast<uint32_t*>(sm + kTm);
   volatile int* bail = reinterpret_cast<volatile int*>(sm + kBail);
   const uint32_t sb = smem_u32(sm);
@@ -247,6 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     mbar_init(last, 1);
     mbar_init(fixed, 32);
+    mbar_init(first, 1);
+    mbar_init(first_fixed, 32);
     fence_mbar_init();
     *bail = 0;
     if (n > 0) {  // the CTA's own rows and the first step's, on their way while it sets up
@@ -280,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (is_k) {
     // =================================================================== dK, dV
     constexpr uint32_t S = 0, DP = 64, P = 128, DS = 160, DVC = 192, DK = 320;  // columns
+    // rows of the first step that see no key: a sequence's first queries, when it has more than keys
+    const int blind = a.causal ? max(0, -lag) - j0 * BQ : 0;
     auto sees_few = [&](int t) {
       return (a.causal ? min(r.lk, (j0 + t + 1) * BQ + lag) : r.lk) <= kFew;
     };
@@ -302,6 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k0 = sdesc_sw128(sb + SmK::K, 16, 1024), v0 = sdesc_sw128(sb + SmK::V, 16, 1024);
       auto scores = [&](int t) {  // S^T = K Q^T
         wait_for(full + t % kQStages, t / kQStages & 1, bail);
+        if (t == 0 && blind > 0) {
+          mbar_arrive(first);
+          wait_for(first_fixed, 0, bail);
+        }
         if (r.lq - (j0 + t) * BQ < BQ) {
           mbar_arrive(last);
           wait_for(fixed, 0, bail);
@@ -357,12 +367,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(drain);
         mbar_wait(drain, 0, kDrainCycles);
       }
-    } else if (warp == 2 && n > 0 && r.lq - (j1 - 1) * BQ < BQ) {
-      // queries past the sequence may hold anything (0 x NaN is NaN): cleared
-      wait_for(last, 0, bail);
-      zero_rows(sm + SmK::ST + (n - 1) % kQStages * SmK::STAGE, kAtomQ, 5, r.lq - (j1 - 1) * BQ, BQ, lane);
-      fence_async_smem();
-      mbar_arrive(fixed);
+    } else if (warp == 2 && n > 0) {
+      // queries that see no key and those past the sequence may hold anything (0 x NaN is NaN):
+      // cleared
+      if (blind > 0) {
+        wait_for(first, 0, bail);
+        zero_rows(sm + SmK::ST, kAtomQ, 5, 0, min(blind, BQ), lane);
+        fence_async_smem();
+        mbar_arrive(first_fixed);
+      }
+      if (r.lq - (j1 - 1) * BQ < BQ) {
+        wait_for(last, 0, bail);
+        zero_rows(sm + SmK::ST + (n - 1) % kQStages * SmK::STAGE, kAtomQ, 5, r.lq - (j1 - 1) * BQ, BQ, lane);
+        fence_async_smem();
+        mbar_arrive(fixed);
+      }
     } else if (warp >= 4) {
       const int g = (warp - 4) / 4, w = warp % 4;
       const uint32_t lanes = tb + (static_cast<uint32_t>(w * 32) << 16);
