@@ -280,8 +280,9 @@ kda_status kda_decode_step(const void *q, const void *k, const void *v, const vo
  *      s_j = scale q . [c_j | k_pe_j],  p = softmax_j(s),  out = sum_j p_j c_j
  *
  * Scores, softmax statistics and sums are fp32; probabilities and score gradients enter
- * the tensor cores as bf16 (score gradients of sequences' first rows, where a query sees at
- * most 384 keys, in two bf16 terms). lse is the natural log of the sum of exponentials. A row
+ * the tensor cores as bf16; score gradients in two bf16 terms in tiles none of whose queries
+ * sees more than 384 keys (dq: 128 queries a tile, dk_nope and dk_pe: 64), so in all of a
+ * sequence of at most 384 keys. lse is the natural log of the sum of exponentials. A row
  * that sees no key has out = 0, lse = -inf and dq = 0 and adds nothing to any gradient,
  * whatever its q and d_out hold. A key or value that is not finite may reach any row of its own
  * sequence, masked from it or not, and never another sequence's; any other query or d_out that

@@ -18,16 +18,25 @@
 //             P^T and dS^T the A operands of dV += P^T dO and dK += dS^T Q
 //   k_pe      the heads' fp32 parts of dk_pe, summed in the heads' order
 //
-// dS enters its products as bf16. Rows that see few keys carry most of a gradient's squares and
-// feel the rounding of out in D the most, so steps whose queries see at most kFew keys add what
-// dS lost, as a second bf16 term. Relative errors of dq against 64 bits (1.66e-3 are the result's
-// own rounding), and the time of packed documents of 156 to 1432 tokens:
-//   kFew                          128      256      384
-//   208 queries of 245 tokens     2.48e-3  1.84e-3  1.84e-3
-//   125 queries of 425 tokens     2.45e-3  2.45e-3  1.77e-3
-//   8 documents of 540 to 655     2.32e-3  2.18e-3  2.09e-3
-//   backward and forward          260 us   263      265      (before few_kernel)
-// From some 400 keys on a row's single term stays below 2.4e-3.
+// dS enters its products as bf16, which brings its products the same error again as rounding the
+// result does (1.66e-3 of the norm; together 2.35e-3, and what the rounding of out does through D on
+// top). Tiles none of whose queries sees more than kFew keys add what dS lost, as a second bf16
+// term: for dQ a tile of 128 queries, for dK a step of 64, so one query's term may be kept in one
+// of the two and not in the other. Rows of few keys carry most of a gradient's squares, so of a
+// sequence's first rows this pays the most. Relative errors of dq and dk_nope against 64 bits, in
+// 1e-3 (causal, 4 heads; lq | lk: queries behind a prefix), and the time of a packed training step
+// of 6 documents of 156 to 1432 tokens:
+//   kFew                  32           128          256          384          512
+//   4 of 245 tokens       2.48 2.45    2.03 2.01    1.81 1.79    1.81 1.79    1.81 1.79
+//   3 of 425              2.42 2.40    2.09 2.07    1.94 1.92    1.81 1.80    1.78 1.76
+//   1000                  2.41 2.36    2.17 2.14    2.06 2.03    1.99 1.96    1.92 1.89
+//   4 of 64 | 320         2.49 2.45    2.49 2.45    2.49 2.45    1.76 1.74    1.76 1.74
+//   125 | 425             2.38 2.36    2.38 2.36    2.38 2.36    2.38 2.03    1.74 1.71
+//   300 | 600             2.42 2.38    2.42 2.38    2.42 2.38    2.42 2.23    2.12 1.93
+//   packed step           264 us       264          269          270          275
+// With 384, sequences of up to 2100 tokens that see themselves are below 2.1e-3 for 2.5 % of a packed
+// step; behind a longer prefix (and without causality from 385 keys on) the single term's 2.4e-3 to
+// 2.5e-3 stay.
 //
 // In both, S of the next step is issued as soon as this step's is in registers, dP likewise,
 // so the products run beside the exponentials.
@@ -42,7 +51,7 @@ namespace {
 constexpr int BM = 128;                    // queries of a dQ CTA, keys of a dK CTA
 constexpr int BQ = 64;                     // query step of a dK CTA, key step of a dQ CTA
 constexpr uint32_t kAtom = BM * 128, kAtomQ = BQ * 128;
-constexpr int kFew = 384;                  // keys up to which dS is kept in two terms
+constexpr int kFew = 384;                  // most keys of a tile whose dS is kept in two terms
 constexpr int kQStages = 3, kKStages = 4, kVStages = 3;
 constexpr int kThreads = 384, kSoft = 256;
 
