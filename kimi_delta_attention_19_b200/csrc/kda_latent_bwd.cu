@@ -96,18 +96,13 @@ __global__ void __launch_bounds__(256) prepare_kernel(AttnArgs a, int64_t tq) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int64_t t = t0 + warp * 4 + 2 * k + lane / 16, row = (t < tq ? t : tq - 1) * a.H + h;
-    x[k] = *reinterpret_cast<const uint4*>(a.dout + row * DV + 8 * (lane % 16));
-    y[k] = *reinterpret_cast<const uint4*>(a.o + row * DV + 8 * (lane % 16));
+    x[k] = ld16(a.dout + row * DV + 8 * (lane % 16));
+    y[k] = ld16(a.o + row * DV + 8 * (lane % 16));
     l[k] = a.lse_in[row];
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, v[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      s += __uint_as_float(u[e] << 16) * __uint_as_float(v[e] << 16) +
-           __uint_as_float(u[e] & 0xffff0000u) * __uint_as_float(v[e] & 0xffff0000u);
+    float s = dot8(x[k], y[k]);
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (lane % 16 == 0)

@@ -23,18 +23,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 // Bounded waits. `bail` is a shared word of the CTA: the first wait that runs out (about a
 // second) sets it, every later wait returns at once, no further copy is issued, and all loops
 // run to their ends (so no named barrier is left short); the CTA then reports kDevWaitTimeout and
