@@ -70,7 +70,7 @@ def _link(lib: str, objs: list[str]) -> None:
 
 # The latent-attention binding's extension module (csrc/latent_host.cpp), for this interpreter
 # and this torch. Without it (no Python.h, no torch headers, another g++) the library is whole and
-# the binding's calls take some 10 us longer, so that it cannot be built is a warning.
+# the binding's calls take the host 5 to 11 us longer, so that it cannot be built is a warning.
 HOST_MODULE = os.path.join(PKG, "_latent_host.so")
 
 

@@ -4,8 +4,9 @@
 // what the kernels take (bf16, on the current GPU, the layouts of include/kda.h), allocates the
 // results and calls the library. Anything else, right or wrong (another device or stream,
 // results of the caller's, a shape that does not fit), is answered with None: latent.py then
-// goes through its own checks, which say what is wrong. For a single token over a short cache
-// the same steps in Python take 11 us, more than the GPU's 9.
+// goes through its own checks, which say what is wrong. In Python the same steps take the host
+// 17 us for a decode and for a forward and 7.5 for a cache write, more than the 14, 7 and 3 that a
+// token over a short cache, a few short prompts and a few tokens take the GPU; here 7.5, 5.8 and 2.6.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
